@@ -364,6 +364,76 @@ pa_status pa_prefill(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_
                      const pa_tensor* block_tables, const pa_tensor* context_lens, const pa_tensor* query_start,
                      int32_t max_query_len, float scale, int32_t num_kv_heads, const pa_opts* opts);
 
+/* ---------------------------------------------------------------------------
+ * Tree attention: speculative decoding's target step.  A draft proposes a
+ * tree of tokens per sequence; the tree's tokens are appended to the cache
+ * (pa_seq_append, pa_reshape_and_cache) and the target model scores all of
+ * them in one step, each seeing the committed context and its own ancestors:
+ *
+ *   sequence i has n_i = query_start[i+1] - query_start[i] drafted tokens at
+ *   cache positions c_i + u, u < n_i (c_i = context_lens[i] - n_i); for row
+ *   r = query_start[i] + j and query head h, g = h / (H / H_kv):
+ *     seen(t) = t < c_i, or t = c_i + u and bit u of tree_mask[r] is set
+ *     s_t = scale * <query[r,h,:], K_i[t, g, :]>
+ *     out[r,h,:] = sum over seen t of softmax(s)_t V_i[t, g, :]
+ *
+ * A row that sees nothing (c_i = 0 and no bit) is zero.  A row sees itself
+ * only if its own bit is set.  A row does not depend on K or V at positions
+ * that it does not see, whatever they hold (NaN included).
+ *
+ * out, query:   [T, H, D] of the cache's dtype, last dim contiguous, strides
+ *               multiples of 16 bytes, 16-byte aligned.  Rows not covered by
+ *               any sequence are left as they were.
+ * k_cache, v_cache: bf16 or fp32, head size 64 or 128 (layout above).
+ * block_tables: [B, max_blocks_per_seq] int32; entries past
+ *               ceil(context_lens[i] / 16) are not read; bad ids set
+ *               PA_DEV_BAD_BLOCK and are replaced by block 0.
+ * context_lens: [B] int32, the drafted tokens included.
+ * query_start:  [B + 1] int32, as for pa_prefill; a sequence whose range does
+ *               not fit (rows outside [0, T), n_i < 0, n_i > context_lens[i],
+ *               n_i > max_query_len, context_lens[i] above the table
+ *               capacity) sets PA_DEV_BAD_CONTEXT and is skipped.
+ * tree_mask:    [T, words] int32, words >= ceil(max_query_len / 32): bit
+ *               u % 32 of word u / 32 of row r is drafted token u of r's
+ *               sequence.  Bits from n_i on are ignored.
+ * max_query_len: host-side bound on every n_i, at most PA_TREE_MAX_QUERY.
+ * scale:        finite and > 0.  H / H_kv in {1, 2, 4, 8}.
+ * opts->partition_tokens: 0 (balanced split over all SMs when the workspace
+ * is at least pa_tree_attention_workspace_bytes, zero-filled before its first
+ * use as for pa_decode; else no split) or -1 (no split); fixed partitions are
+ * PA_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+#define PA_TREE_MAX_QUERY 1024
+pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                            const pa_tensor* block_tables, const pa_tensor* context_lens,
+                            const pa_tensor* query_start, const pa_tensor* tree_mask, int32_t max_query_len,
+                            float scale, int32_t num_kv_heads, const pa_opts* opts);
+/* Workspace bytes of the balanced split for these sizes on the current
+ * device (an upper bound over the cache types). */
+pa_status pa_tree_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                                            int32_t max_query_len, size_t* bytes_out);
+
+/* Commit of the accepted path: after the target step, the K/V of the accepted
+ * drafted tokens move to the positions right after the context, in path
+ * order, so that the sequence continues as if they had been decoded one by
+ * one; pa_seq_truncate then gives the rejected tokens' slots back.
+ *
+ *   for k < num_accepted[i], every kv head: K/V at position c_i + k of
+ *   sequence i  <-  K/V at position c_i + accepted[i][k]
+ *
+ * accepted:     [B, P] int32, strictly ascending in [0, n_i) over its first
+ *               num_accepted[i] <= min(P, n_i) entries (children follow their
+ *               parents in a draft); the rest is not read.
+ * num_accepted: [B] int32; 0 moves nothing.
+ * Other arguments as pa_tree_attention, any cache dtype.  A sequence whose
+ * path, draft or table does not fit sets PA_DEV_BAD_CONTEXT, a bad block id
+ * PA_DEV_BAD_BLOCK; nothing of that sequence moves.  Bit copy.  The drafted
+ * positions must lie in blocks that no other sequence of the call holds
+ * (the allocator's appends ensure it). */
+pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                         const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* accepted,
+                         const pa_tensor* num_accepted, const pa_opts* opts);
+
 /* Workspace bytes pa_decode needs on the current device for these sizes and
  * this partition_tokens setting (0 = auto/balanced, >0 = fixed, -1 = none),
  * header included; 0 for -1.  Departs from the survey's sketch

@@ -26,7 +26,8 @@ __all__ = [
     "pa_decode_workspace_bytes", "pa_decode_no_alloc", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_prefill",
     "pa_decode_cascade", "pa_decode_cascade_workspace_bytes", "PreparedCall", "prepare_reshape_and_cache",
     "prepare_decode", "prepare_decode_cascade", "prepare_reshape_and_cache_fp8", "prepare_decode_fp8",
-    "pa_swap_blocks", "pa_set_decode_tuning", "pa_get_device_status", "pa_debug_wait_selftest",
+    "pa_tree_attention", "pa_tree_attention_workspace_bytes", "pa_tree_commit", "prepare_tree_attention",
+    "prepare_tree_commit", "pa_swap_blocks", "pa_set_decode_tuning", "pa_get_device_status", "pa_debug_wait_selftest",
     "Allocator", "library",
 ]
 
@@ -209,6 +210,42 @@ def pa_prefill(out, query, k_cache, v_cache, block_tables, context_lens, query_s
                                       int(num_kv_heads), ctypes.byref(o)), "pa_prefill")
 
 
+def pa_tree_attention(out, query, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask,
+                      max_query_len: int, scale: float, num_kv_heads: int, workspace=None, partition_tokens: int = 0,
+                      stream=None, timeout_ms: int = 0) -> None:
+    """Attention of a tree of drafted tokens: writes out [T, H, D]; row r of
+    sequence i sees the sequence's committed context and the drafted tokens
+    whose bits are set in ``tree_mask`` (int32 [T, words]).  ``workspace``: at
+    least ``pa_tree_attention_workspace_bytes`` bytes, zero-filled before first
+    use (without one the context of a sequence is not split)."""
+    args = (out, query, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask)
+    ts = [_tensor(x) for x in args]
+    with _on_device(args + (workspace,)):
+        o = _opts(stream, workspace, partition_tokens, timeout_ms)
+        _check(_lib_handle.pa_tree_attention(*[ctypes.byref(t) for t in ts], int(max_query_len),
+                                             ctypes.c_float(scale), int(num_kv_heads), ctypes.byref(o)),
+               "pa_tree_attention")
+
+
+def pa_tree_attention_workspace_bytes(num_heads: int, num_kv_heads: int, head_size: int, max_query_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib_handle.pa_tree_attention_workspace_bytes(num_heads, num_kv_heads, head_size, max_query_len,
+                                                         ctypes.byref(n)), "pa_tree_attention_workspace_bytes")
+    return int(n.value)
+
+
+def pa_tree_commit(k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted,
+                   stream=None) -> None:
+    """Move the K/V of each sequence's accepted drafted tokens (``accepted``
+    int32 [B, P], strictly ascending; ``num_accepted`` int32 [B]) to the
+    positions right after its committed context."""
+    args = (k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted)
+    ts = [_tensor(x) for x in args]
+    with _on_device(args):
+        o = _opts(stream)
+        _check(_lib_handle.pa_tree_commit(*[ctypes.byref(t) for t in ts], ctypes.byref(o)), "pa_tree_commit")
+
+
 def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None) -> None:
     """Quantizing cache write into an FP8 (torch.float8_e4m3fn) cache: each
     value is stored as the e4m3 code of value / scale[kv head]."""
@@ -364,6 +401,25 @@ def prepare_decode_cascade(out, query, k_cache, v_cache, block_tables, context_l
     return PreparedCall("pa_decode_cascade", args,
                         [ctypes.c_int32(int(max_group_size)), ctypes.c_float(scale), ctypes.c_int32(int(num_kv_heads))],
                         _opts(stream, workspace, partition_tokens, timeout_ms), args + (workspace,))
+
+
+def prepare_tree_attention(out, query, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask,
+                           max_query_len: int, scale: float, num_kv_heads: int, workspace=None,
+                           partition_tokens: int = 0, stream=None, timeout_ms: int = 0) -> PreparedCall:
+    """pa_tree_attention, prepared (see PreparedCall)."""
+    args = (out, query, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask)
+    _device_index(args + (workspace,))
+    return PreparedCall("pa_tree_attention", args,
+                        [ctypes.c_int32(int(max_query_len)), ctypes.c_float(scale), ctypes.c_int32(int(num_kv_heads))],
+                        _opts(stream, workspace, partition_tokens, timeout_ms), args + (workspace,))
+
+
+def prepare_tree_commit(k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted,
+                        stream=None) -> PreparedCall:
+    """pa_tree_commit, prepared (see PreparedCall)."""
+    args = (k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted)
+    _device_index(args)
+    return PreparedCall("pa_tree_commit", args, [], _opts(stream), args)
 
 
 # ---------------------------------------------------------------------------

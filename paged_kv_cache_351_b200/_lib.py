@@ -80,6 +80,9 @@ SIGNATURES = {
     "pa_decode_cascade": (c_int32, [_T, _T, _T, _T, _T, _T, _T, _T, c_int32, c_float, c_int32, _O]),
     "pa_decode_cascade_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
                                                     POINTER(c_size_t)]),
+    "pa_tree_attention": (c_int32, [_T, _T, _T, _T, _T, _T, _T, _T, c_int32, c_float, c_int32, _O]),
+    "pa_tree_attention_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, POINTER(c_size_t)]),
+    "pa_tree_commit": (c_int32, [_T, _T, _T, _T, _T, _T, _T, _O]),
     "pa_alloc_prefix_groups": (c_int32, [_A, _I64P, c_int32, c_int32, _I32P, _I32P, _I32P]),
     "pa_set_decode_tuning": (c_int32, [c_int32, c_int32, c_int32]),
     "pa_alloc_create": (c_int32, [c_int32, c_int32, _I32P, POINTER(_A)]),

@@ -19,6 +19,7 @@
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
 #include "pa_prefill.cuh"
+#include "pa_tree.cuh"
 
 namespace {
 
@@ -973,6 +974,197 @@ pa_status pa_prefill(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_
     default:
       return run_prefill<8>(tq, tk, tv, a, max_query_len, int(Hkv), s, dev);
   }
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// tree attention and the accepted path of a tree of drafted tokens
+// ---------------------------------------------------------------------------
+
+// [B] or [B + 1] int32, contiguous.
+pa_status check_i32_vec(const pa_tensor* t, int64_t n) {
+  if (t == nullptr || t->ndim != 1 || t->dtype != PA_I32 || t->shape[0] != n) return PA_ERR_INVALID_ARG;
+  if (n > 0 && (t->data == nullptr || (n > 1 && t->stride[0] != 1) || (reinterpret_cast<uintptr_t>(t->data) & 3u)))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+// [n, m] of 32-bit elements, last dim contiguous, rows at least m apart.
+pa_status check_rows2(const pa_tensor* t, int32_t dtype, int64_t n) {
+  if (t == nullptr || t->ndim != 2 || t->dtype != dtype || t->shape[0] != n || t->shape[1] < 0)
+    return PA_ERR_INVALID_ARG;
+  if (n == 0 || t->shape[1] == 0) return PA_OK;
+  if (t->data == nullptr || (t->shape[1] > 1 && t->stride[1] != 1) || (n > 1 && t->stride[0] < t->shape[1]) ||
+      (reinterpret_cast<uintptr_t>(t->data) & 3u))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+// Launch shape of a tree attention: R query rows per unit, KT keys per tile,
+// worker CTAs, and the warps that count shares in.
+struct TreePlan {
+  int R, KT, workers, warps;
+};
+
+constexpr int kTreeSimtCtas = 4;  // CTAs per SM of the CUDA-core kernel (its shared memory allows 5)
+
+pa_status tree_plan(TreePlan* p) {
+  DeviceInfo di;
+  const pa_status st = device_info(&di, nullptr);
+  if (st != PA_OK) return st;
+  *p = TreePlan{pa::kTsRows, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps};
+  return PA_OK;
+}
+
+// Header, shares (two slots per worker), their (max, denominator) pairs.
+size_t tree_ws_bytes(const TreePlan& p, int64_t D) {
+  return kWsHeader + align_up(size_t(2) * p.workers * p.R * D * 4, 256) + align_up(size_t(2) * p.workers * p.R * 8, 256);
+}
+
+template <typename T, int D>
+pa_status run_tree_simt(const pa::TreeArgs& a, const TreePlan& p, cudaStream_t s, int dev) {
+  static std::atomic<size_t> smem_limit[kMaxDevices];
+  auto kern = pa::tree_simt_kernel<T, D>;
+  constexpr size_t smem = pa::tree_simt_smem<D>();
+  if (!raise_smem_limit(kern, smem, dev, smem_limit)) return PA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(unsigned(p.workers)), dim3(pa::kTsWarps * 32), smem, s, true, a) != cudaSuccess)
+    return launch_status();
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_tree_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_heads, int32_t head_size,
+                                            int32_t max_query_len, size_t* bytes_out) {
+  if (bytes_out == nullptr || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 || num_heads % num_kv_heads ||
+      max_query_len < 0)
+    return PA_ERR_INVALID_ARG;
+  *bytes_out = 0;
+  TreePlan p;
+  const pa_status st = tree_plan(&p);
+  if (st != PA_OK) return st;
+  *bytes_out = tree_ws_bytes(p, head_size);
+  return PA_OK;
+}
+
+pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                            const pa_tensor* block_tables, const pa_tensor* context_lens,
+                            const pa_tensor* query_start, const pa_tensor* tree_mask, int32_t max_query_len,
+                            float scale, int32_t num_kv_heads, const pa_opts* opts) {
+  pa_status st = check_pair(k_cache, v_cache);
+  if (st != PA_OK) return st;
+  const int64_t NB = k_cache->shape[0], Hkv = k_cache->shape[1], D = k_cache->shape[3];
+  const int32_t dt = k_cache->dtype;
+  if (dt == PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  if (num_kv_heads != Hkv) return PA_ERR_INVALID_ARG;
+  if (query == nullptr || query->ndim != 3) return PA_ERR_INVALID_ARG;
+  const int64_t T = query->shape[0], H = query->shape[1];
+  if (T < 0 || H <= 0 || H % Hkv) return PA_ERR_INVALID_ARG;
+  if ((st = check_rows3(query, dt, T, H, D)) != PA_OK) return st;
+  if ((st = check_rows3(out, dt, T, H, D)) != PA_OK) return st;
+  if (context_lens == nullptr || context_lens->ndim != 1) return PA_ERR_INVALID_ARG;
+  const int64_t B = context_lens->shape[0];
+  if (B < 0) return PA_ERR_INVALID_ARG;
+  if ((st = check_i32_vec(context_lens, B)) != PA_OK) return st;
+  if ((st = check_i32_vec(query_start, B + 1)) != PA_OK) return st;
+  if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
+  if ((st = check_rows2(tree_mask, PA_I32, T)) != PA_OK) return st;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  if (max_query_len < 0 || (T > 0 && max_query_len == 0) || max_query_len > T) return PA_ERR_INVALID_ARG;
+  if (tree_mask->shape[1] < (int64_t(max_query_len) + 31) / 32) return PA_ERR_INVALID_ARG;
+  if (opts && (opts->partition_tokens < -1)) return PA_ERR_INVALID_ARG;
+  if (opts && opts->partition_tokens > 0) return PA_ERR_UNSUPPORTED;
+  if (opts && opts->workspace != nullptr && (reinterpret_cast<uintptr_t>(opts->workspace) & 255u))
+    return PA_ERR_INVALID_ARG;
+  const int64_t G = H / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
+  if (max_query_len > PA_TREE_MAX_QUERY) return PA_ERR_UNSUPPORTED;
+  const int64_t max_nb = block_tables->shape[1];
+  if (B > 65535 || T >= (int64_t(1) << 31) || max_nb * 16 > INT32_MAX || tree_mask->shape[1] > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return PA_OK;
+
+  TreePlan p;
+  if ((st = tree_plan(&p)) != PA_OK) return st;
+  // the tile list is indexed with 32 bits
+  const int64_t tiles_max = B * Hkv * ((max_query_len * G + p.R - 1) / p.R) * ((max_nb * 16 + p.KT - 1) / p.KT);
+  if (tiles_max > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  pa::TreeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.out = out->data;
+  a.q = query->data;
+  a.kc = k_cache->data;
+  a.vc = v_cache->data;
+  a.bt = static_cast<const int32_t*>(block_tables->data);
+  a.ctx = static_cast<const int32_t*>(context_lens->data);
+  a.qs = static_cast<const int32_t*>(query_start->data);
+  a.mask = static_cast<const uint32_t*>(tree_mask->data);
+  a.q_st = query->stride[0], a.q_sh = query->stride[1];
+  a.o_st = out->stride[0], a.o_sh = out->stride[1];
+  a.bt_stride = B > 1 ? block_tables->stride[0] : 0;
+  a.mask_stride = T > 1 ? tree_mask->stride[0] : 0;
+  a.B = int32_t(B), a.T = int32_t(T), a.Hkv = int32_t(Hkv), a.G = int32_t(G), a.max_nb = int32_t(max_nb);
+  a.num_blocks = int32_t(NB), a.words = int32_t(tree_mask->shape[1]), a.max_q = max_query_len;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.timeout_ns = timeout_of(opts);
+  const bool split = opts && opts->partition_tokens == 0 && opts->workspace != nullptr &&
+                     opts->workspace_bytes >= tree_ws_bytes(p, D);
+  a.split = split ? 1 : 0;
+  if (split) {
+    char* w = static_cast<char*>(opts->workspace);
+    a.cnt = reinterpret_cast<unsigned int*>(w);
+    a.sh_o = reinterpret_cast<float*>(w + kWsHeader);
+    a.sh_ml = reinterpret_cast<float2*>(w + kWsHeader + align_up(size_t(2) * p.workers * p.R * D * 4, 256));
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
+  cudaStream_t s = stream_of(opts);
+  if (dt == PA_BF16 && D == 128) return run_tree_simt<__nv_bfloat16, 128>(a, p, s, dev);
+  if (dt == PA_BF16 && D == 64) return run_tree_simt<__nv_bfloat16, 64>(a, p, s, dev);
+  if (dt == PA_F32 && D == 128) return run_tree_simt<float, 128>(a, p, s, dev);
+  if (dt == PA_F32 && D == 64) return run_tree_simt<float, 64>(a, p, s, dev);
+  return PA_ERR_UNSUPPORTED;
+}
+
+pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                         const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* accepted,
+                         const pa_tensor* num_accepted, const pa_opts* opts) {
+  pa_status st = check_pair(k_cache, v_cache);
+  if (st != PA_OK) return st;
+  if (context_lens == nullptr || context_lens->ndim != 1) return PA_ERR_INVALID_ARG;
+  const int64_t B = context_lens->shape[0];
+  if (B < 0) return PA_ERR_INVALID_ARG;
+  if ((st = check_i32_vec(context_lens, B)) != PA_OK) return st;
+  if ((st = check_i32_vec(query_start, B + 1)) != PA_OK) return st;
+  if ((st = check_i32_vec(num_accepted, B)) != PA_OK) return st;
+  if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
+  if ((st = check_rows2(accepted, PA_I32, B)) != PA_OK) return st;
+  const int64_t max_nb = block_tables->shape[1];
+  if (B > 65535 || max_nb * 16 > INT32_MAX || accepted->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B == 0) return PA_OK;
+  pa::CommitArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.kc = static_cast<uint4*>(k_cache->data);
+  a.vc = static_cast<uint4*>(v_cache->data);
+  a.bt = static_cast<const int32_t*>(block_tables->data);
+  a.ctx = static_cast<const int32_t*>(context_lens->data);
+  a.qs = static_cast<const int32_t*>(query_start->data);
+  a.acc = static_cast<const int32_t*>(accepted->data);
+  a.count = static_cast<const int32_t*>(num_accepted->data);
+  a.bt_stride = B > 1 ? block_tables->stride[0] : 0;
+  a.acc_stride = B > 1 ? accepted->stride[0] : 0;
+  a.B = int32_t(B), a.Hkv = int32_t(k_cache->shape[1]), a.max_nb = int32_t(max_nb);
+  a.num_blocks = int32_t(k_cache->shape[0]), a.P = int32_t(accepted->shape[1]);
+  a.vpr = int32_t(k_cache->shape[3] * esize(k_cache->dtype) / 16);
+  const int per_seq = a.Hkv * 2 * a.vpr;
+  const cudaError_t err = launch_pdl(pa::tree_commit_kernel, dim3(unsigned((per_seq + 127) / 128), unsigned(B)),
+                                     dim3(128), 0, stream_of(opts), true, a);
+  return err == cudaSuccess ? PA_OK : launch_status();
 }
 
 pa_status pa_get_device_status(const pa_opts* opts, uint32_t* bits_out) {

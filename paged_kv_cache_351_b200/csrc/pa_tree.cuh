@@ -1,0 +1,451 @@
+// Speculative decoding over the paged cache (sm_100a): attention of a tree
+// of drafted tokens, and the move of the accepted path's K/V.
+//
+// Tree attention.  Sequence i brings n_i drafted tokens, rows query_start[i]
+// .. query_start[i+1] - 1, whose K/V already sit at cache positions c_i ..
+// c_i + n_i - 1 (c_i = context_lens[i] - n_i).  Row j sees every committed
+// key t < c_i and the drafted key c_i + u if bit u of its mask row is set:
+//   out[r, h] = sum_{t visible} softmax_t(scale * <q[r,h], K_i[t, g]>) V_i[t, g],
+//   g = h / G;  a row that sees nothing is zero.
+//
+// Work list (both kernels below).  A unit is (sequence, kv head, tile of R
+// query rows), the rows being the unit's drafted tokens times the G query
+// heads of the kv head, so that a K/V page is read once for all of them; it
+// is a run of key tiles of KT tokens.  The workers (CTAs) of a persistent
+// grid take equal contiguous ranges of the flattened tile list, whatever the
+// mix of lengths; a unit cut by a range boundary leaves one share per worker
+// (output before the division, running max, denominator), and the warp that
+// counts in the unit's last tiles merges the shares of its rows in worker
+// order.  Nobody waits for anybody, the result does not depend on who came
+// last, and every counter is zero again when the launch ends.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_decode.cuh"
+
+namespace pa {
+
+struct TreeArgs {
+  void* out;            // [T, H, D]
+  const void* q;        // [T, H, D]
+  const void* kc;
+  const void* vc;
+  const int32_t* bt;    // [B, max_nb]
+  const int32_t* ctx;   // [B] tokens in the cache, the drafted ones included
+  const int32_t* qs;    // [B + 1] first row of each sequence
+  const uint32_t* mask; // [T, words]
+  int64_t q_st, q_sh, o_st, o_sh, bt_stride, mask_stride;
+  int32_t B, T, Hkv, G, max_nb, num_blocks, words, max_q;
+  float scale_log2;  // scale * log2(e)
+  int32_t split;     // 1: units may be cut between workers (shares below)
+  float* sh_o;       // shares: two slots per worker, [R][D] floats each
+  float2* sh_ml;     // [R] (running max in log2 units, denominator)
+  unsigned int* cnt; // per worker and warp: tiles of the unit that starts there counted in so far
+  uint64_t timeout_ns;
+};
+
+// The drafted rows of sequence i (n = 0: none, or a range that does not fit).
+struct TreeSeq {
+  int q0, n, c0;  // first row, rows, committed tokens
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int i) {
+  const int64_t q0 = __ldg(a.qs + i), q1 = __ldg(a.qs + i + 1);
+  const int ctx = __ldg(a.ctx + i);
+  const int64_t n = q1 - q0;
+  if (q0 < 0 || n < 0 || q1 > a.T || n > ctx || ctx > a.max_nb * kBS || n > a.max_q) {
+    if (blockIdx.x == 0) flag(PA_DEV_BAD_CONTEXT);
+    return TreeSeq{0, 0, 0};
+  }
+  return TreeSeq{int(q0), int(n), ctx - int(n)};
+}
+
+// Position in the flattened tile list: sequence, unit of the sequence (kv
+// head major, row tile minor), key tile of the unit.
+struct TreePos {
+  int i, u, p;
+  int units, nt;  // units of the sequence, key tiles of each
+  TreeSeq s;
+};
+
+template <int R, int KT>
+__device__ __forceinline__ void tree_shape(const TreeArgs& a, TreePos& x) {
+  x.s = tree_seq(a, x.i);
+  x.units = a.Hkv * ((x.s.n * a.G + R - 1) / R);
+  x.nt = x.s.n > 0 ? (x.s.c0 + x.s.n + KT - 1) / KT : 0;
+}
+
+// Next unit of the list (x.p = 0), skipping sequences without drafted rows.
+template <int R, int KT>
+__device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreePos& x) {
+  x.p = 0;
+  if (++x.u < x.units) return;
+  x.u = 0;
+  do {
+    ++x.i;
+    if (x.i >= a.B) return;
+    tree_shape<R, KT>(a, x);
+  } while (x.units == 0);
+}
+
+// Whole block: this worker's range [lo, hi) of the tile list, the list's
+// length, and the position of lo.  smem: 40 ints.
+struct TreeRange {
+  int64_t W, lo, hi;
+  TreePos at;
+};
+
+template <int R, int KT>
+__device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
+  const int nthr = blockDim.x;
+  const int per = (a.B + nthr - 1) / nthr;
+  const int i0 = min(a.B, int(threadIdx.x) * per), i1 = min(a.B, i0 + per);
+  int local = 0;
+  for (int i = i0; i < i1; ++i) {
+    TreePos x;
+    x.i = i;
+    tree_shape<R, KT>(a, x);
+    local += x.units * x.nt;
+  }
+  int total;
+  const int first = block_exclusive_scan(local, smem, &total);
+  TreeRange r;
+  r.W = total;
+  const int64_t N = gridDim.x, w = blockIdx.x;
+  r.lo = (w * r.W + N - 1) / N;
+  r.hi = ((w + 1) * r.W + N - 1) / N;
+  // the thread that owns the tile finds its sequence; without a split both
+  // ends move down to the start of their unit
+  for (int e = 0; e < 2; ++e) {
+    const int64_t b = e == 0 ? r.lo : r.hi;
+    if (b < r.W && b >= first && b < first + local) {
+      int base = first;
+      for (int i = i0; i < i1; ++i) {
+        TreePos x;
+        x.i = i;
+        tree_shape<R, KT>(a, x);
+        const int t = x.units * x.nt;
+        if (b < base + t) {
+          const int off = int(b) - base;
+          smem[32 + 4 * e + 0] = i;
+          smem[32 + 4 * e + 1] = off / x.nt;
+          smem[32 + 4 * e + 2] = a.split ? off % x.nt : 0;
+          smem[32 + 4 * e + 3] = a.split ? 0 : off % x.nt;
+          break;
+        }
+        base += t;
+      }
+    }
+  }
+  __syncthreads();
+  if (r.lo < r.W) {
+    r.at.i = smem[32];
+    r.at.u = smem[33];
+    r.at.p = smem[34];
+    tree_shape<R, KT>(a, r.at);
+    r.lo -= smem[35];
+  }
+  if (r.hi < r.W) r.hi -= smem[39];
+  __syncthreads();
+  return r;
+}
+
+// Bits of the 32 drafted keys u0 .. u0 + 31 that row `row` sees (u0 may be
+// negative: committed keys are all seen, and so are no keys past the draft).
+__device__ __forceinline__ uint32_t tree_word(const TreeArgs& a, int64_t row, int n, int w) {
+  if (w < 0 || w >= a.words || w * 32 >= n) return 0u;
+  const uint32_t x = __ldg(a.mask + row * a.mask_stride + w);
+  const int left = n - w * 32;
+  return left >= 32 ? x : x & ((1u << left) - 1u);
+}
+
+__device__ __forceinline__ uint32_t tree_seen32(const TreeArgs& a, int64_t row, int n, int u0) {
+  if (u0 >= 0) {
+    const int w = u0 >> 5, sh = u0 & 31;
+    return __funnelshift_r(tree_word(a, row, n, w), sh ? tree_word(a, row, n, w + 1) : 0u, sh);
+  }
+  if (u0 <= -32) return 0xffffffffu;
+  const int k = -u0;  // committed keys in the low k bits, 1 <= k <= 31
+  return (tree_word(a, row, n, 0) << k) | ((1u << k) - 1u);
+}
+
+// ---- CUDA-core kernel ----------------------------------------------------
+// fp32 caches: products and sums in fp32, no tensor-core rounding.  R = 16
+// query rows per CTA, four to a warp; a tile of 32 keys is staged in shared
+// memory as fp32.  Scores: lane = key, the query row broadcast from shared
+// memory (K rows padded to D + 4 floats, so that 16-byte reads of 32
+// consecutive rows touch every bank once per phase).  Weighted sum: lane =
+// D / 32 dims, the probabilities broadcast by shuffles.
+constexpr int kTsRows = 16;
+constexpr int kTsKeys = 32;
+constexpr int kTsWarps = 4;
+
+template <int D>
+constexpr size_t tree_simt_smem() {
+  return size_t(kTsKeys * (D + 4) + kTsKeys * D + kTsRows * D) * 4 + 64 * 4;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs a) {
+  constexpr int EPV = 16 / int(sizeof(T)), VPR = D / EPV, PER = D / 32, RW = kTsRows / kTsWarps;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* Ks = reinterpret_cast<float*>(smem);
+  float* Vs = Ks + kTsKeys * (D + 4);
+  float* Qs = Vs + kTsKeys * D;
+  int* scratch = reinterpret_cast<int*>(Qs + kTsRows * D);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  const TreeRange rg = tree_range<kTsRows, kTsKeys>(a, scratch);
+  TreePos x = rg.at;
+  const int64_t N = gridDim.x;
+  const uint4* kc = static_cast<const uint4*>(a.kc);
+  const uint4* vc = static_cast<const uint4*>(a.vc);
+
+  for (int64_t cx = rg.lo; cx < rg.hi;) {
+    // ---- one segment: this worker's tiles [x.p, pe) of one unit ----
+    const int rts = x.units / a.Hkv;
+    const int kvh = x.u / rts, r0 = (x.u % rts) * kTsRows;
+    const int rows = min(kTsRows, x.s.n * a.G - r0);
+    const int pe = int(x.nt - x.p < rg.hi - cx ? x.nt : x.p + (rg.hi - cx));
+    const int kv_len = x.s.c0 + x.s.n;
+    for (int e = threadIdx.x; e < kTsRows * VPR; e += blockDim.x) {
+      const int r = e / VPR, c = e % VPR;
+      float f[EPV];
+#pragma unroll
+      for (int k = 0; k < EPV; ++k) f[k] = 0.f;
+      if (r < rows) {
+        const int tok = (r0 + r) / a.G, j = (r0 + r) % a.G;
+        Elem<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (x.s.q0 + tok) * a.q_st +
+                                                        (kvh * a.G + j) * a.q_sh + c * EPV),
+                        f);
+      }
+#pragma unroll
+      for (int k = 0; k < EPV; ++k) Qs[r * D + c * EPV + k] = f[k] * a.scale_log2;
+    }
+    float o[RW][PER], m[RW], l[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[r][e] = 0.f;
+    }
+    for (int p = x.p; p < pe; ++p) {
+      const int key0 = p * kTsKeys;
+      __syncthreads();  // the previous tile (and the query rows) are no longer in use / are complete
+      for (int e = threadIdx.x; e < kTsKeys * VPR; e += blockDim.x) {
+        const int t = e / VPR, c = e % VPR;
+        float kf[EPV], vf[EPV];
+#pragma unroll
+        for (int k = 0; k < EPV; ++k) kf[k] = vf[k] = 0.f;
+        if (key0 + t < kv_len) {
+          int blk = __ldg(a.bt + int64_t(x.i) * a.bt_stride + (key0 + t) / kBS);
+          if (unsigned(blk) >= unsigned(a.num_blocks)) {
+            flag(PA_DEV_BAD_BLOCK);
+            blk = 0;
+          }
+          const int64_t off = ((int64_t(blk) * a.Hkv + kvh) * kBS + (key0 + t) % kBS) * VPR + c;
+          Elem<T>::unpack(__ldg(kc + off), kf);
+          Elem<T>::unpack(__ldg(vc + off), vf);
+        }
+#pragma unroll
+        for (int k = 0; k < EPV; ++k) {
+          Ks[t * (D + 4) + c * EPV + k] = kf[k];
+          Vs[t * D + c * EPV + k] = vf[k];
+        }
+      }
+      __syncthreads();
+      if (warp * RW >= rows) continue;  // none of this warp's rows exist
+      float s[RW];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) s[r] = 0.f;
+      const float4* kr = reinterpret_cast<const float4*>(Ks + lane * (D + 4));
+#pragma unroll 4
+      for (int d = 0; d < D / 4; ++d) {
+        const float4 k4 = kr[d];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          const float4 q4 = reinterpret_cast<const float4*>(Qs + (warp * RW + r) * D)[d];
+          s[r] = fmaf(q4.x, k4.x, s[r]);
+          s[r] = fmaf(q4.y, k4.y, s[r]);
+          s[r] = fmaf(q4.z, k4.z, s[r]);
+          s[r] = fmaf(q4.w, k4.w, s[r]);
+        }
+      }
+      const bool tree = key0 + kTsKeys > x.s.c0;  // some keys are drafted, or past the end
+      uint32_t seen[RW];
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const int row = r0 + warp * RW + r;
+        seen[r] = 0xffffffffu;
+        if (tree) seen[r] = row < x.s.n * a.G ? tree_seen32(a, x.s.q0 + row / a.G, x.s.n, key0 - x.s.c0) : 0u;
+        const bool vis = (seen[r] >> lane) & 1u;
+        if (!vis) s[r] = -INFINITY;
+        float mx = s[r];
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        const float mn = fmaxf(m[r], mx);
+        const float al = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+        m[r] = mn;
+        s[r] = vis ? ex2(s[r] - mn) : 0.f;
+        l[r] = l[r] * al + s[r];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[r][e] *= al;
+      }
+      const int nk = min(kTsKeys, kv_len - key0);
+      for (int t = 0; t < nk; ++t) {
+        float v[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = Vs[t * D + lane * PER + e];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          const float pt = __shfl_sync(0xffffffffu, s[r], t);
+          if (!((seen[r] >> t) & 1u)) continue;  // a masked V may hold anything
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[r][e] = fmaf(pt, v[e], o[r][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
+
+    // ---- the segment's result: rows of the output, or a share of a cut unit ----
+    const bool whole = x.p == 0 && pe == x.nt;
+    const int64_t unit0 = cx - x.p;  // the unit's first tile in the list
+    bool write = whole;
+    if (!whole) {
+      const int64_t wa = unit0 * N / rg.W;
+      const int64_t slot = share_slot(blockIdx.x, wa);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        if (warp * RW + r >= rows) continue;
+        const int64_t row = slot * kTsRows + warp * RW + r;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) a.sh_o[row * D + lane * PER + e] = o[r][e];
+        if (lane == 0) a.sh_ml[row] = make_float2(m[r], l[r]);
+      }
+      write = share_done(a.cnt + wa * kTsWarps + warp, pe - x.p, x.nt);
+      if (write) {
+        const int64_t wb = (unit0 + x.nt - 1) * N / rg.W;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          m[r] = -INFINITY;
+          l[r] = 0.f;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[r][e] = 0.f;
+          if (warp * RW + r >= rows) continue;
+          for (int64_t k = wa; k <= wb; ++k) {
+            if (worker_empty(k, rg.W, N)) continue;
+            const int64_t row = share_slot(k, wa) * kTsRows + warp * RW + r;
+            const float2 ml = __ldcg(a.sh_ml + row);
+            if (ml.y == 0.f) continue;  // a share that saw nothing
+            const float mn = fmaxf(m[r], ml.x);
+            const float al = ex2(m[r] - mn), be = ex2(ml.x - mn);
+            m[r] = mn;
+            l[r] = l[r] * al + ml.y * be;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+              o[r][e] = o[r][e] * al + (be == 0.f ? 0.f : __ldcg(a.sh_o + row * D + lane * PER + e) * be);
+          }
+        }
+      }
+    }
+    if (write) {
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        if (warp * RW + r >= rows) continue;
+        const int row = r0 + warp * RW + r;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // 0: the row sees nothing
+        float y[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) y[e] = l[r] == 0.f ? 0.f : o[r][e] * inv;
+        store_out_small<T, PER>(static_cast<T*>(a.out) + (x.s.q0 + row / a.G) * a.o_st +
+                                    (kvh * a.G + row % a.G) * a.o_sh + lane * PER,
+                                y);
+      }
+    }
+    cx += pe - x.p;
+    tree_next_unit<kTsRows, kTsKeys>(a, x);
+    __syncthreads();  // the query rows are replaced by the next segment's
+  }
+}
+
+// ---- accepted path --------------------------------------------------------
+// cache position c_i + k  <-  position c_i + accepted[i][k], k < count[i], for
+// K and V of every head.  The accepted indices ascend strictly (children
+// follow their parents in a draft), so accepted[k] >= k and a row is only
+// ever overwritten after it was read, in the order k = 0, 1, ...  One thread
+// owns one 16-byte column of a (sequence, head) and walks its path: no two
+// threads touch the same bytes, so the walk needs no synchronisation.  Pure
+// copy; bound by the latency of two dependent rounds (the path and the block
+// ids, then the rows), so kCommitBatch rows are loaded at once.
+constexpr int kCommitBatch = 8;
+
+struct CommitArgs {
+  uint4* kc;
+  uint4* vc;
+  const int32_t* bt;
+  const int32_t* ctx;
+  const int32_t* qs;
+  const int32_t* acc;
+  const int32_t* count;
+  int64_t bt_stride, acc_stride;
+  int32_t B, Hkv, max_nb, num_blocks, P, vpr;
+};
+
+__global__ void __launch_bounds__(128) tree_commit_kernel(const CommitArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_seq = a.Hkv * 2 * a.vpr;
+  const int i = blockIdx.y;
+  const int id = blockIdx.x * blockDim.x + threadIdx.x;
+  if (id >= per_seq) return;
+  const int c = id % a.vpr, kv = (id / a.vpr) & 1, h = id / (2 * a.vpr);
+  const int count = __ldg(a.count + i);
+  if (count == 0) return;
+  const int64_t n = int64_t(__ldg(a.qs + i + 1)) - __ldg(a.qs + i);
+  const int ctx = __ldg(a.ctx + i);
+  const int32_t* acc = a.acc + int64_t(i) * a.acc_stride;
+  bool ok = count > 0 && count <= a.P && n >= count && n <= ctx && ctx <= a.max_nb * kBS;
+  int last = -1;
+  for (int k = 0; ok && k < count; ++k) {
+    const int u = __ldg(acc + k);
+    ok = u > last && u < n;
+    last = u;
+  }
+  if (!ok) {
+    if (id == 0) flag(PA_DEV_BAD_CONTEXT);
+    return;
+  }
+  const int c0 = ctx - int(n);
+  const int32_t* bt = a.bt + int64_t(i) * a.bt_stride;
+  // every block of the path is in the pool, or nothing of the sequence moves
+  for (int b = c0 / kBS; b <= (c0 + last) / kBS; ++b) {
+    if (unsigned(__ldg(bt + b)) >= unsigned(a.num_blocks)) {
+      if (id == 0) flag(PA_DEV_BAD_BLOCK);
+      return;
+    }
+  }
+  uint4* cache = kv ? a.vc : a.kc;
+  auto at = [&](int pos) {
+    return cache + ((int64_t(__ldg(bt + pos / kBS)) * a.Hkv + h) * kBS + pos % kBS) * a.vpr + c;
+  };
+  for (int k0 = 0; k0 < count; k0 += kCommitBatch) {
+    uint4 row[kCommitBatch];
+    int u[kCommitBatch];
+#pragma unroll
+    for (int k = 0; k < kCommitBatch; ++k) {
+      u[k] = k0 + k < count ? __ldg(acc + k0 + k) : k0 + k;
+      if (u[k] != k0 + k) row[k] = __ldcg(at(c0 + u[k]));
+    }
+#pragma unroll
+    for (int k = 0; k < kCommitBatch; ++k)
+      if (u[k] != k0 + k) *at(c0 + k0 + k) = row[k];
+  }
+}
+
+}  // namespace pa
