@@ -434,6 +434,74 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
                          const pa_tensor* context_lens, const pa_tensor* query_start, const pa_tensor* accepted,
                          const pa_tensor* num_accepted, const pa_opts* opts);
 
+/* ---------------------------------------------------------------------------
+ * Scored decode: pa_decode (or pa_decode_fp8, for an e4m3 cache) that also
+ * adds every cached token's attention weight to an accumulator, from which
+ * pa_evict chooses the tokens that stay when a sequence exceeds its budget.
+ *
+ *   out[i,h,:] as pa_decode;  with w[i,h,t] = softmax(s_i,h)_t,
+ *   scores[i,g,t] += sum over the heads h of group g of w[i,h,t],  t < context_lens[i]
+ *
+ * scores:       [B, H_kv, S] fp32, last dim contiguous, any row strides;
+ *               position t of a row belongs to token t of the sequence (not
+ *               to its slot, so forks of a prompt score it separately).  A
+ *               sequence longer than S sets PA_DEV_BAD_CONTEXT, and its
+ *               tokens from S on are not scored.  Entries from
+ *               context_lens[i] on are left as they were.  Sums are fp32,
+ *               in the order of the heads; results do not vary from run to
+ *               run on the same split.
+ * k_scale, v_scale: [H_kv] fp32 for an e4m3 cache (query and out bf16), NULL
+ *               otherwise.
+ * Other arguments and dtypes as pa_decode.  opts->workspace: required, of
+ * pa_decode_scored_workspace_bytes bytes, zero-filled before its first use;
+ * opts->partition_tokens: 0 (balanced split) or -1 (no split); fixed
+ * partitions are PA_ERR_UNSUPPORTED.  After a call that timed out the
+ * scores, like the outputs, are unspecified.  Two launches.
+ * ------------------------------------------------------------------------- */
+pa_status pa_decode_scored(pa_tensor* out, pa_tensor* scores, const pa_tensor* query, const pa_tensor* k_cache,
+                           const pa_tensor* v_cache, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                           float scale, int32_t num_kv_heads, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                           const pa_opts* opts);
+/* Workspace bytes of pa_decode_scored on the current device (an upper bound
+ * over the cache types).  It holds one fp32 logit per (sequence, head, table
+ * position): size the block tables to the batch. */
+pa_status pa_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_size, int32_t max_blocks_per_seq, int32_t partition_tokens,
+                                           size_t* bytes_out);
+
+/* ---------------------------------------------------------------------------
+ * Eviction by accumulated weight: sequence i keeps K = min(keep_lens[i],
+ * context_lens[i]) of its tokens, chosen per kv head: the R = min(num_recent,
+ * K) newest, the S0 = min(num_sink, K - R) first, and of the others the
+ * K - R - S0 with the largest scores (ties to the lower position; NaN ranks
+ * with -infinity).  The kept tokens' K/V, in their order, become positions
+ * 0 .. K - 1 of the blocks that dst_tables names (fresh blocks from
+ * pa_seq_compact: out of place, so blocks shared with forks or with the
+ * prefix cache stay as they are).  Keys carry their rotary positions, so
+ * attention over the compacted cache needs nothing else.
+ *
+ *   kept_out[i,g,j]   = position of kept token j (ascending), -1 for j >= K
+ *   scores_out[i,g,j] = scores[i,g,kept_out[i,g,j]], 0 for j >= K
+ *   K/V at position j of dst_tables[i], head g = K/V at position
+ *   kept_out[i,g,j] of block_tables[i], head g
+ *
+ * k_cache, v_cache: any dtype (bit copy), source and destination blocks.
+ * block_tables, dst_tables: [B, *] int32; only entries that cover
+ *               context_lens[i] (K) tokens are read.  A block outside the
+ *               pool sets PA_DEV_BAD_BLOCK and its rows are not moved.  A
+ *               destination block must not be any sequence's source block.
+ * scores, scores_out: [B, H_kv, S] and [B, H_kv, S'] fp32, not overlapping.
+ * keep_lens:    [B] int32.  kept_out: [B, H_kv, P] int32.
+ * A sequence with context_lens[i] or keep_lens[i] below 0, more tokens than
+ * its table or S holds, or K above P, S' or the destination table's capacity
+ * sets PA_DEV_BAD_CONTEXT and is skipped (nothing of it is written).
+ * No workspace.  Two launches.
+ * ------------------------------------------------------------------------- */
+pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                   const pa_tensor* context_lens, const pa_tensor* scores, const pa_tensor* dst_tables,
+                   const pa_tensor* keep_lens, int32_t num_sink, int32_t num_recent, pa_tensor* scores_out,
+                   pa_tensor* kept_out, const pa_opts* opts);
+
 /* Workspace bytes pa_decode needs on the current device for these sizes and
  * this partition_tokens setting (0 = auto/balanced, >0 = fixed, -1 = none),
  * header included; 0 for -1.  Departs from the survey's sketch
@@ -566,6 +634,25 @@ int32_t pa_alloc_num_host_free(const pa_allocator* a);
 /* Host blocks of a swapped-out sequence, in table order (else
  * PA_ERR_INVALID_ARG). */
 pa_status pa_seq_host_table(const pa_allocator* a, int64_t seq_id, int32_t* out, int32_t cap, int32_t* n_out);
+/* Shortens a sequence to its first new_len tokens (0 <= new_len <= length;
+ * e.g. the rejected end of a draft): blocks past ceil(new_len / bs) lose one
+ * reference in table order.  A kept block stays shared as it was, so a later
+ * append into its rest copies it first while it has other holders; if it is
+ * registered for prefix reuse and not shared, that append gives up its key
+ * (and its registered children's).  Append drafted tokens with pa_seq_append
+ * (ids unknown), so that no block of a tree is ever registered. */
+pa_status pa_seq_truncate(pa_allocator* a, int64_t seq_id, int32_t new_len);
+/* Gives each of n distinct sequences ceil(new_lens[r] / bs) fresh blocks (0 <=
+ * new_lens[r] <= its length) as its whole table, written to row r of
+ * tables_out [n, max_blocks] (padded with -1): the destination of pa_evict.
+ * Every fresh block is taken, in order, before any sequence's old blocks lose
+ * their reference (in order, in table order), so no destination of the batch
+ * is a source of it.  All or nothing (PA_ERR_OUT_OF_BLOCKS changes nothing).
+ * The sequences' token ids become unknown.  Later calls may hand the old
+ * blocks out again, so launch the pa_evict that reads them before anything
+ * that writes them. */
+pa_status pa_seq_compact(pa_allocator* a, const int64_t* seq_ids, const int32_t* new_lens, int32_t n,
+                         int32_t* tables_out, int32_t max_blocks);
 /* Releases the sequence's blocks (device, or host if swapped out) and
  * forgets the id; an unknown id (e.g. a second free) is PA_ERR_INVALID_ARG. */
 pa_status pa_seq_free(pa_allocator* a, int64_t seq_id);

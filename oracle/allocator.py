@@ -270,6 +270,46 @@ class BlockAllocator:
         self._tokens[seq] = tokens[:len(hits) * bs]
         return len(hits) * bs
 
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Keep the first ``new_len`` tokens; blocks past them lose a reference."""
+        self._check_resident(seq)
+        if not 0 <= new_len <= self._len[seq]:
+            raise AllocatorError("bad length")
+        keep = -(-new_len // self.block_size)
+        table = self._table[seq]
+        for b in table[keep:]:
+            self._release(b)
+        self._table[seq] = table[:keep]
+        self._len[seq] = new_len
+        if self._tokens.get(seq) is not None:
+            self._tokens[seq] = self._tokens[seq][:new_len]
+
+    def compact(self, seqs: Sequence[int], new_lens: Sequence[int]) -> List[List[int]]:
+        """Fresh blocks for ``new_lens`` tokens of each sequence; then the old
+        blocks of all of them lose a reference."""
+        if len(set(seqs)) != len(seqs):
+            raise AllocatorError("a sequence appears twice")
+        need = 0
+        for seq, n in zip(seqs, new_lens):
+            self._check_resident(seq)
+            if not 0 <= n <= self._len[seq]:
+                raise AllocatorError("bad length")
+            need += -(-n // self.block_size)
+        if need > self.num_free():
+            raise OutOfBlocks(f"{need} blocks, {self.num_free()} free")
+        fresh = []
+        for n in new_lens:
+            fresh.append([self._take_block() for _ in range(-(-n // self.block_size))])
+            for b in fresh[-1]:
+                self._ref[b] = 1
+        for seq, n, table in zip(seqs, new_lens, fresh):
+            for b in self._table[seq]:
+                self._release(b)
+            self._table[seq] = list(table)
+            self._len[seq] = n
+            self._tokens[seq] = None
+        return fresh
+
     def _blocks_needed(self, seq: int, n: int) -> int:
         bs = self.block_size
         pos = self._len[seq]
@@ -321,6 +361,9 @@ class BlockAllocator:
                     self._ref[last] -= 1
                     table[-1] = b
                     cow.append((last, b))
+                elif last in self._key_of:
+                    # the rest of a registered block is about to be written
+                    self._unregister(last)
             slots.append(table[pos // bs] * bs + pos % bs)
             self._len[seq] = pos + 1
             if toks is not None:

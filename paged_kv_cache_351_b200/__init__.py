@@ -27,7 +27,8 @@ __all__ = [
     "pa_decode_cascade", "pa_decode_cascade_workspace_bytes", "PreparedCall", "prepare_reshape_and_cache",
     "prepare_decode", "prepare_decode_cascade", "prepare_reshape_and_cache_fp8", "prepare_decode_fp8",
     "pa_tree_attention", "pa_tree_attention_workspace_bytes", "pa_tree_commit", "prepare_tree_attention",
-    "prepare_tree_commit", "pa_swap_blocks", "pa_set_decode_tuning", "pa_get_device_status", "pa_debug_wait_selftest",
+    "prepare_tree_commit", "pa_decode_scored", "pa_decode_scored_workspace_bytes", "pa_evict",
+    "prepare_decode_scored", "prepare_evict", "pa_swap_blocks", "pa_set_decode_tuning", "pa_get_device_status", "pa_debug_wait_selftest",
     "Allocator", "library",
 ]
 
@@ -246,6 +247,48 @@ def pa_tree_commit(k_cache, v_cache, block_tables, context_lens, query_start, ac
         _check(_lib_handle.pa_tree_commit(*[ctypes.byref(t) for t in ts], ctypes.byref(o)), "pa_tree_commit")
 
 
+def pa_decode_scored(out, scores, query, k_cache, v_cache, block_tables, context_lens, scale: float,
+                     num_kv_heads: int, workspace, k_scale=None, v_scale=None, partition_tokens: int = 0,
+                     stream=None, timeout_ms: int = 0) -> None:
+    """pa_decode (over an FP8 cache with ``k_scale`` and ``v_scale``) that
+    also adds each cached token's attention weight, summed over the heads of
+    its group, to ``scores`` (float32 [B, H_kv, S]).  ``workspace``: at least
+    ``pa_decode_scored_workspace_bytes`` bytes, zero-filled before first use."""
+    args = (out, scores, query, k_cache, v_cache, block_tables, context_lens)
+    ts = [_tensor(x) for x in args]
+    sc = [_tensor(x) if x is not None else None for x in (k_scale, v_scale)]
+    with _on_device(args + (k_scale, v_scale, workspace)):
+        o = _opts(stream, workspace, partition_tokens, timeout_ms)
+        _check(_lib_handle.pa_decode_scored(*[ctypes.byref(t) for t in ts], ctypes.c_float(scale), int(num_kv_heads),
+                                            *[ctypes.byref(t) if t is not None else None for t in sc],
+                                            ctypes.byref(o)), "pa_decode_scored")
+
+
+def pa_decode_scored_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_size: int,
+                                     max_blocks_per_seq: int, partition_tokens: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib_handle.pa_decode_scored_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_size,
+                                                        max_blocks_per_seq, partition_tokens, ctypes.byref(n)),
+           "pa_decode_scored_workspace_bytes")
+    return int(n.value)
+
+
+def pa_evict(k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens, num_sink: int,
+             num_recent: int, scores_out, kept_out, stream=None) -> None:
+    """Keep ``keep_lens[i]`` tokens of each sequence (the ``num_sink`` first,
+    the ``num_recent`` newest, then the largest ``scores``), chosen per kv
+    head, and move their K/V in order into the blocks of ``dst_tables``;
+    ``scores_out`` gets their scores (then zeros), ``kept_out`` their
+    positions (then -1)."""
+    args = (k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens)
+    ts = [_tensor(x) for x in args]
+    outs = [_tensor(x) for x in (scores_out, kept_out)]
+    with _on_device(args + (scores_out, kept_out)):
+        o = _opts(stream)
+        _check(_lib_handle.pa_evict(*[ctypes.byref(t) for t in ts], int(num_sink), int(num_recent),
+                                    *[ctypes.byref(t) for t in outs], ctypes.byref(o)), "pa_evict")
+
+
 def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None) -> None:
     """Quantizing cache write into an FP8 (torch.float8_e4m3fn) cache: each
     value is stored as the e4m3 code of value / scale[kv head]."""
@@ -422,6 +465,34 @@ def prepare_tree_commit(k_cache, v_cache, block_tables, context_lens, query_star
     return PreparedCall("pa_tree_commit", args, [], _opts(stream), args)
 
 
+def prepare_decode_scored(out, scores, query, k_cache, v_cache, block_tables, context_lens, scale: float,
+                          num_kv_heads: int, workspace, k_scale=None, v_scale=None, partition_tokens: int = 0,
+                          stream=None, timeout_ms: int = 0) -> PreparedCall:
+    """pa_decode_scored, prepared (see PreparedCall)."""
+    args = (out, scores, query, k_cache, v_cache, block_tables, context_lens)
+    _device_index(args + (k_scale, v_scale, workspace))
+    call = PreparedCall("pa_decode_scored", args, [ctypes.c_float(scale), ctypes.c_int32(int(num_kv_heads))],
+                        _opts(stream, workspace, partition_tokens, timeout_ms), args + (k_scale, v_scale, workspace))
+    # the two scale descriptors (or NULL) go between num_kv_heads and opts
+    call._scales = [_tensor(t) if t is not None else None for t in (k_scale, v_scale)]
+    call._args = call._args[:-1] + [ctypes.byref(t) if t is not None else None
+                                    for t in call._scales] + call._args[-1:]
+    return call
+
+
+def prepare_evict(k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens, num_sink: int,
+                  num_recent: int, scores_out, kept_out, stream=None) -> PreparedCall:
+    """pa_evict, prepared (see PreparedCall)."""
+    args = (k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens)
+    _device_index(args + (scores_out, kept_out))
+    call = PreparedCall("pa_evict", args, [ctypes.c_int32(int(num_sink)), ctypes.c_int32(int(num_recent))],
+                        _opts(stream), args + (scores_out, kept_out))
+    # the two outputs' descriptors go between num_recent and opts
+    call._outs = [_tensor(t) for t in (scores_out, kept_out)]
+    call._args = call._args[:-1] + [ctypes.byref(t) for t in call._outs] + call._args[-1:]
+    return call
+
+
 # ---------------------------------------------------------------------------
 # host allocator
 # ---------------------------------------------------------------------------
@@ -546,6 +617,23 @@ class Allocator:
         _check(_lib_handle.pa_alloc_evictable(self._h, _i32p(out), self.num_blocks, ctypes.byref(n)),
                "pa_alloc_evictable")
         return out[: n.value].tolist()
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Shorten a sequence to its first ``new_len`` tokens (rejected drafted tokens)."""
+        _check(_lib_handle.pa_seq_truncate(self._h, seq, int(new_len)), "pa_seq_truncate")
+
+    def compact(self, seqs: Sequence[int], new_lens: Sequence[int], max_blocks: int):
+        """Give each sequence fresh blocks for ``new_lens[k]`` tokens (the
+        destination of ``pa_evict``), then release the old ones of all of
+        them; returns the new tables, int32 [n, max_blocks] padded with -1."""
+        ids = np.ascontiguousarray(np.asarray(seqs, np.int64))
+        lens = np.ascontiguousarray(np.asarray(new_lens, np.int32))
+        if ids.shape != lens.shape or ids.ndim != 1:
+            raise ValueError("one new length per sequence")
+        out = np.zeros((max(len(ids), 1), max(max_blocks, 1)), np.int32)
+        _check(_lib_handle.pa_seq_compact(self._h, _i64p(ids), _i32p(lens), len(ids), _i32p(out), max_blocks),
+               "pa_seq_compact")
+        return out.reshape(-1)[: len(ids) * max_blocks].reshape(len(ids), max_blocks)
 
     def free(self, seq: int) -> None:
         _check(_lib_handle.pa_seq_free(self._h, seq), "pa_seq_free")

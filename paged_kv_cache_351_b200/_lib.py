@@ -83,6 +83,10 @@ SIGNATURES = {
     "pa_tree_attention": (c_int32, [_T, _T, _T, _T, _T, _T, _T, _T, c_int32, c_float, c_int32, _O]),
     "pa_tree_attention_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, POINTER(c_size_t)]),
     "pa_tree_commit": (c_int32, [_T, _T, _T, _T, _T, _T, _T, _O]),
+    "pa_decode_scored": (c_int32, [_T, _T, _T, _T, _T, _T, _T, c_float, c_int32, _T, _T, _O]),
+    "pa_decode_scored_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                   POINTER(c_size_t)]),
+    "pa_evict": (c_int32, [_T, _T, _T, _T, _T, _T, _T, c_int32, c_int32, _T, _T, _O]),
     "pa_alloc_prefix_groups": (c_int32, [_A, _I64P, c_int32, c_int32, _I32P, _I32P, _I32P]),
     "pa_set_decode_tuning": (c_int32, [c_int32, c_int32, c_int32]),
     "pa_alloc_create": (c_int32, [c_int32, c_int32, _I32P, POINTER(_A)]),
@@ -100,6 +104,8 @@ SIGNATURES = {
     "pa_alloc_num_host_free": (c_int32, [_A]),
     "pa_seq_host_table": (c_int32, [_A, c_int64, _I32P, c_int32, _I32P]),
     "pa_swap_blocks": (c_int32, [_T, _T, _T, _T, _T, _O]),
+    "pa_seq_truncate": (c_int32, [_A, c_int64, c_int32]),
+    "pa_seq_compact": (c_int32, [_A, _I64P, _I32P, c_int32, _I32P, c_int32]),
     "pa_seq_free": (c_int32, [_A, c_int64]),
     "pa_seq_len": (c_int32, [_A, c_int64, _I32P]),
     "pa_seq_block_table": (c_int32, [_A, c_int64, _I32P, c_int32, _I32P]),

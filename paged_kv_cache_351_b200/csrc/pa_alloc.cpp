@@ -217,6 +217,10 @@ struct pa_allocator {
             cow_pair[1] = b;
           }
           ++cows;
+        } else if (reg[last]) {
+          // a registered block of which a truncation left a part: the slots
+          // behind that part are about to be written, so its key is given up
+          unregister(last);
         }
       }
       slots[k] = static_cast<int64_t>(s.table[pos / bs]) * bs + pos % bs;
@@ -458,6 +462,67 @@ pa_status pa_seq_fork(pa_allocator* a, int64_t parent, int64_t child) {
     Seq c = it->second;  // copy before emplace may rehash
     for (int32_t b : c.table) a->ref[b] += 1;
     a->seqs.emplace(child, std::move(c));
+    return PA_OK;
+  });
+}
+
+pa_status pa_seq_truncate(pa_allocator* a, int64_t seq_id, int32_t new_len) {
+  return no_throw([&]() -> pa_status {
+    if (a == nullptr) return PA_ERR_INVALID_ARG;
+    auto it = a->seqs.find(seq_id);
+    if (it == a->seqs.end() || it->second.swapped || new_len < 0 || new_len > it->second.len)
+      return PA_ERR_INVALID_ARG;
+    Seq& s = it->second;
+    const size_t keep = (static_cast<size_t>(new_len) + a->block_size - 1) / a->block_size;
+    for (size_t k = keep; k < s.table.size(); ++k) a->release(s.table[k]);
+    s.table.resize(keep);
+    s.len = new_len;
+    if (s.tracked) s.tokens.resize(new_len);
+    return PA_OK;
+  });
+}
+
+pa_status pa_seq_compact(pa_allocator* a, const int64_t* seq_ids, const int32_t* new_lens, int32_t n,
+                         int32_t* tables_out, int32_t max_blocks) {
+  return no_throw([&]() -> pa_status {
+    if (a == nullptr || n < 0 || max_blocks < 0 || (n > 0 && (seq_ids == nullptr || new_lens == nullptr)))
+      return PA_ERR_INVALID_ARG;
+    int64_t need = 0;
+    std::vector<Seq*> ss(n);
+    std::set<int64_t> seen;
+    for (int32_t r = 0; r < n; ++r) {
+      auto it = a->seqs.find(seq_ids[r]);
+      if (it == a->seqs.end() || it->second.swapped || new_lens[r] < 0 || new_lens[r] > it->second.len ||
+          !seen.insert(seq_ids[r]).second)
+        return PA_ERR_INVALID_ARG;
+      const int64_t k = (static_cast<int64_t>(new_lens[r]) + a->block_size - 1) / a->block_size;
+      if (k > max_blocks || (k > 0 && tables_out == nullptr)) return PA_ERR_INVALID_ARG;
+      need += k;
+      ss[r] = &it->second;
+    }
+    if (need > a->available()) return PA_ERR_OUT_OF_BLOCKS;
+    // every fresh block is taken before any old one is released: no
+    // destination of the batch is a source of it
+    std::vector<std::vector<int32_t>> fresh(n);
+    for (int32_t r = 0; r < n; ++r) {
+      fresh[r].resize((static_cast<size_t>(new_lens[r]) + a->block_size - 1) / a->block_size);
+      for (int32_t& b : fresh[r]) {
+        b = a->take_block();
+        a->ref[b] = 1;
+      }
+      int32_t* row = tables_out + static_cast<int64_t>(r) * max_blocks;
+      for (int32_t k = 0; k < max_blocks && tables_out != nullptr; ++k)
+        row[k] = k < static_cast<int32_t>(fresh[r].size()) ? fresh[r][k] : -1;
+    }
+    for (int32_t r = 0; r < n; ++r) {
+      Seq& s = *ss[r];
+      for (int32_t b : s.table) a->release(b);
+      s.table.swap(fresh[r]);
+      s.len = new_lens[r];
+      s.tracked = false;
+      s.tokens.clear();
+      s.tokens.shrink_to_fit();
+    }
     return PA_OK;
   });
 }

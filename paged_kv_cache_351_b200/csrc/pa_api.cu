@@ -20,6 +20,7 @@
 #include "pa_decode.cuh"
 #include "pa_prefill.cuh"
 #include "pa_tree.cuh"
+#include "pa_evict.cuh"
 
 namespace {
 
@@ -733,7 +734,7 @@ static pa_status launch_kind(const DecodeCall& dc, int G, const pa::DecodeArgs& 
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
   const int32_t dt = dc.dt;
   const int64_t D = dc.D;
-  if constexpr (CK == pa::kPlain) {
+  if constexpr (CK != pa::kGroup) {
     if (dt == PA_BF16 && D == 128) return dispatch_group<__nv_bfloat16, __nv_bfloat16, 128, CK>(G, a, plan, s, dev);
     if (dt == PA_BF16 && D == 64) return dispatch_group<__nv_bfloat16, __nv_bfloat16, 64, CK>(G, a, plan, s, dev);
     if (dt == PA_F32 && D == 64) return dispatch_group<float, float, 64, CK>(G, a, plan, s, dev);
@@ -1164,6 +1165,186 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
   const int per_seq = a.Hkv * 2 * a.vpr;
   const cudaError_t err = launch_pdl(pa::tree_commit_kernel, dim3(unsigned((per_seq + 127) / 128), unsigned(B)),
                                      dim3(128), 0, stream_of(opts), true, a);
+  return err == cudaSuccess ? PA_OK : launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// scored decode and eviction
+// ---------------------------------------------------------------------------
+
+// Scored-decode workspace: [header][shares of the split (none for -1)]
+// [log-sum-exps, B x H][logits, B x H_kv x capacity x G].
+size_t scored_lse_off(int64_t workers, int64_t G, int64_t D, int32_t part) {
+  return kWsHeader + (part == 0 ? shares_bytes(workers, G, D) : 0);
+}
+size_t scored_ws_bytes(int64_t B, int64_t H, int64_t cap, size_t lse_off) {
+  return lse_off + align_up(size_t(B * H) * 4, 256) + align_up(size_t(B * H) * size_t(cap) * 4, 256);
+}
+
+// [n0, n1, n2] fp32 or int32, last dim contiguous, rows at least n2 apart.
+pa_status check_rowbuf3(const pa_tensor* t, int32_t dtype, int64_t n0, int64_t n1) {
+  if (t == nullptr || t->ndim != 3 || t->dtype != dtype || t->shape[0] != n0 || t->shape[1] != n1 || t->shape[2] < 0)
+    return PA_ERR_INVALID_ARG;
+  if (n0 == 0 || n1 == 0 || t->shape[2] == 0) return PA_OK;
+  if (t->data == nullptr || (reinterpret_cast<uintptr_t>(t->data) & 3u) || (t->shape[2] > 1 && t->stride[2] != 1) ||
+      (n1 > 1 && t->stride[1] < t->shape[2]) || (n0 > 1 && t->stride[0] < t->shape[2]))
+    return PA_ERR_INVALID_ARG;
+  return t->shape[2] > INT32_MAX ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+template <int G>
+cudaError_t run_accumulate(const pa::AccumArgs& a, dim3 grid, cudaStream_t s) {
+  return launch_pdl(pa::accumulate_scores_kernel<G>, grid, dim3(256), 0, s, true, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_size, int32_t max_blocks_per_seq, int32_t partition_tokens,
+                                           size_t* bytes_out) {
+  if (bytes_out == nullptr || num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+      max_blocks_per_seq < 0 || num_heads % num_kv_heads)
+    return PA_ERR_INVALID_ARG;
+  *bytes_out = 0;
+  if (partition_tokens != 0 && partition_tokens != -1)
+    return partition_tokens > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+  DeviceInfo di;
+  pa_status st = device_info(&di, nullptr);
+  if (st != PA_OK) return st;
+  const int G = num_heads / num_kv_heads;
+  // an upper bound over cache types, as for pa_decode
+  const int64_t workers = int64_t(di.sms) * g_tuning.ctas_per_sm *
+                          (g_tuning.warps ? g_tuning.warps : std::max(default_warps(G, false), default_warps(G, true)));
+  *bytes_out = scored_ws_bytes(num_seqs, num_heads, int64_t(max_blocks_per_seq) * pa::kBS,
+                               scored_lse_off(workers, G, head_size, partition_tokens));
+  return PA_OK;
+}
+
+pa_status pa_decode_scored(pa_tensor* out, pa_tensor* scores, const pa_tensor* query, const pa_tensor* k_cache,
+                           const pa_tensor* v_cache, const pa_tensor* block_tables, const pa_tensor* context_lens,
+                           float scale, int32_t num_kv_heads, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                           const pa_opts* opts) {
+  if (k_cache == nullptr) return PA_ERR_INVALID_ARG;
+  if (k_cache->dtype != PA_FP8_E4M3 && (k_scale != nullptr || v_scale != nullptr)) return PA_ERR_INVALID_ARG;
+  DecodeCall dc;
+  pa_status st = decode_prepare(out, query, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
+                                k_scale, v_scale, opts, &dc);
+  if (st != PA_OK) return st;
+  if ((st = check_rowbuf3(scores, PA_F32, dc.B, dc.Hkv)) != PA_OK) return st;
+  const int32_t part = opts ? opts->partition_tokens : 0;
+  if (part > 0) return PA_ERR_UNSUPPORTED;
+  if (dc.B == 0) return PA_OK;
+  if (opts == nullptr || opts->workspace == nullptr) return PA_ERR_INVALID_ARG;
+  DecodePlan plan;
+  st = plan_decode(dc.dt, int(dc.G), dc.B, 0, dc.B, dc.H, dc.D, dc.max_nb, part,
+                   opts->workspace_bytes > kWsHeader ? opts->workspace_bytes - kWsHeader : 0, true, &plan);
+  if (st != PA_OK) return st;
+  if (part == 0 && plan.mode != pa::kBalanced) return PA_ERR_INVALID_ARG;  // the workspace is too small
+  const int64_t cap = dc.max_nb * pa::kBS;
+  const size_t lse_off = scored_lse_off(int64_t(plan.grid) * plan.warps, dc.G, dc.D, part);
+  if (opts->workspace_bytes < scored_ws_bytes(dc.B, dc.H, cap, lse_off)) return PA_ERR_INVALID_ARG;
+  pa::DecodeArgs a = dc.a;
+  char* w = static_cast<char*>(opts->workspace);
+  if (plan.mode == pa::kBalanced) place_shares(&a, opts->workspace, kWsHeader, plan, dc.G, dc.D);
+  a.lse2 = reinterpret_cast<float*>(w + lse_off);
+  a.logits = reinterpret_cast<float*>(w + lse_off + align_up(size_t(dc.B * dc.H) * 4, 256));
+  cudaStream_t s = stream_of(opts);
+  if ((st = launch_kind<pa::kScored>(dc, int(dc.G), a, plan, s)) != PA_OK) return st;
+  if (cap == 0) return PA_OK;
+
+  DeviceInfo di;
+  if ((st = device_info(&di, nullptr)) != PA_OK) return st;
+  pa::AccumArgs c;
+  c.logits = a.logits;
+  c.lse = a.lse2;
+  c.scores = static_cast<float*>(scores->data);
+  c.ctx = a.ctx;
+  c.s_sb = dc.B > 1 ? scores->stride[0] : 0;
+  c.s_sh = dc.Hkv > 1 ? scores->stride[1] : 0;
+  c.B = int32_t(dc.B), c.Hkv = int32_t(dc.Hkv), c.cap = int32_t(cap), c.S = int32_t(scores->shape[2]);
+  // enough blocks for 8 per SM, each striding over its row's tokens
+  const int64_t rows = dc.B * dc.Hkv;
+  int64_t gx = (int64_t(di.sms) * 8 + rows - 1) / rows;
+  gx = std::min<int64_t>(gx, (cap + 255) / 256);
+  const dim3 grid(unsigned(std::max<int64_t>(gx, 1)), unsigned(dc.Hkv), unsigned(dc.B));
+  cudaError_t err;
+  switch (dc.G) {
+    case 1:
+      err = run_accumulate<1>(c, grid, s);
+      break;
+    case 2:
+      err = run_accumulate<2>(c, grid, s);
+      break;
+    case 4:
+      err = run_accumulate<4>(c, grid, s);
+      break;
+    default:
+      err = run_accumulate<8>(c, grid, s);
+      break;
+  }
+  return err == cudaSuccess ? PA_OK : launch_status();
+}
+
+pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                   const pa_tensor* context_lens, const pa_tensor* scores, const pa_tensor* dst_tables,
+                   const pa_tensor* keep_lens, int32_t num_sink, int32_t num_recent, pa_tensor* scores_out,
+                   pa_tensor* kept_out, const pa_opts* opts) {
+  pa_status st = check_pair(k_cache, v_cache);
+  if (st != PA_OK) return st;
+  const int64_t Hkv = k_cache->shape[1];
+  if (context_lens == nullptr || context_lens->ndim != 1) return PA_ERR_INVALID_ARG;
+  const int64_t B = context_lens->shape[0];
+  if (B < 0 || num_sink < 0 || num_recent < 0) return PA_ERR_INVALID_ARG;
+  if ((st = check_i32_vec(context_lens, B)) != PA_OK) return st;
+  if ((st = check_i32_vec(keep_lens, B)) != PA_OK) return st;
+  if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
+  if ((st = check_rows2(dst_tables, PA_I32, B)) != PA_OK) return st;
+  if ((st = check_rowbuf3(scores, PA_F32, B, Hkv)) != PA_OK) return st;
+  if ((st = check_rowbuf3(scores_out, PA_F32, B, Hkv)) != PA_OK) return st;
+  if ((st = check_rowbuf3(kept_out, PA_I32, B, Hkv)) != PA_OK) return st;
+  const int64_t max_nb = block_tables->shape[1], dst_nb = dst_tables->shape[1];
+  if (B > 65535 || max_nb * 16 > INT32_MAX || dst_nb * 16 > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B == 0) return PA_OK;
+  // the rows are compacted out of place
+  if (scores_out->data == scores->data && scores->shape[2] > 0 && scores_out->shape[2] > 0) return PA_ERR_INVALID_ARG;
+  DeviceInfo di;
+  if ((st = device_info(&di, nullptr)) != PA_OK) return st;
+  pa::EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.scores = static_cast<const float*>(scores->data);
+  a.scores_out = static_cast<float*>(scores_out->data);
+  a.kept = static_cast<int32_t*>(kept_out->data);
+  a.ctx = static_cast<const int32_t*>(context_lens->data);
+  a.keep = static_cast<const int32_t*>(keep_lens->data);
+  a.bt = static_cast<const int32_t*>(block_tables->data);
+  a.dt = static_cast<const int32_t*>(dst_tables->data);
+  a.kc = static_cast<uint4*>(k_cache->data);
+  a.vc = static_cast<uint4*>(v_cache->data);
+  auto stride = [](const pa_tensor* t, int d) { return t->shape[d] > 1 ? t->stride[d] : 0; };
+  a.s_sb = stride(scores, 0), a.s_sh = stride(scores, 1);
+  a.o_sb = stride(scores_out, 0), a.o_sh = stride(scores_out, 1);
+  a.k_sb = stride(kept_out, 0), a.k_sh = stride(kept_out, 1);
+  a.bt_stride = stride(block_tables, 0), a.dt_stride = stride(dst_tables, 0);
+  a.B = int32_t(B), a.Hkv = int32_t(Hkv), a.max_nb = int32_t(max_nb), a.dst_nb = int32_t(dst_nb);
+  a.num_blocks = int32_t(k_cache->shape[0]);
+  a.S = int32_t(scores->shape[2]), a.So = int32_t(scores_out->shape[2]), a.P = int32_t(kept_out->shape[2]);
+  a.sink = num_sink, a.recent = num_recent;
+  a.vpr = int32_t(k_cache->shape[3] * esize(k_cache->dtype) / 16);
+  cudaStream_t s = stream_of(opts);
+  if (launch_pdl(pa::evict_select_kernel, dim3(unsigned(Hkv), unsigned(B)), dim3(pa::kSelThreads), 0, s, true, a) !=
+      cudaSuccess)
+    return launch_status();
+  const int64_t rows = B * Hkv;
+  int64_t gx = (int64_t(di.sms) * 16 + rows - 1) / rows;
+  gx = std::min<int64_t>(gx, (int64_t(a.P) * a.vpr + 255) / 256);
+  const cudaError_t err = launch_pdl(pa::evict_move_kernel, dim3(unsigned(std::max<int64_t>(gx, 1)), unsigned(Hkv),
+                                     unsigned(B)), dim3(256), 0, s, true, a);
   return err == cudaSuccess ? PA_OK : launch_status();
 }
 

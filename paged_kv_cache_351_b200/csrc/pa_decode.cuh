@@ -99,6 +99,10 @@ struct DecodeArgs {
   int32_t n_groups;
   int32_t grp_members;  // most members a group may have (a group row carries members x g_real query rows)
   int32_t g_real;       // query heads per kv head
+  // Scored decode: every logit (log2 units, [B][H_kv][max_nb * 16][G]) and
+  // each row's log-sum-exp (log2 units, [B][H]), for the accumulation pass.
+  float* logits;
+  float* lse2;
 };
 
 // Decode kinds: a plain decode, or a shared-prefix decode.  In the latter a
@@ -107,8 +111,9 @@ struct DecodeArgs {
 // blocks, which every member's rows attend, followed by each member's own
 // remaining blocks, which only that member's rows attend (the other rows are
 // masked).  A shared page is thus read once for the whole group, and each
-// member's output is complete at the row's end: no second pass.
-enum DecodeKind : int { kPlain = 0, kGroup = 1 };
+// member's output is complete at the row's end: no second pass.  A scored
+// decode is a plain one that also leaves its logits and log-sum-exps.
+enum DecodeKind : int { kPlain = 0, kGroup = 1, kScored = 2 };
 
 // Tkv: cache element type (fp32, bf16 or e4m3 codes); Tq: query/output type.
 template <typename Tkv, typename Tq, int D, int G>
@@ -904,6 +909,13 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
           if constexpr (CK == kGroup) {  // a row (head) that does not attend this page
             if (tig < alo || tig >= ahi) t0 = t1 = -INFINITY;
           }
+          if constexpr (CK == kScored) {
+            if (tig < G) {
+              float* lg = a.logits + ((int64_t(cc.i) * Hkv + cc.g) * ctx_cap + cc.p * kBS) * G + tig;
+              lg[gr * G] = t0;
+              lg[(gr + 8) * G] = t1;
+            }
+          }
           float pm = fmaxf(t0, t1);
 #pragma unroll
           for (int msk = 4; msk < 32; msk <<= 1) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, msk));
@@ -943,6 +955,11 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
           if constexpr (CK == kGroup) {  // rows (heads) that do not attend this page
             if (2 * tig < alo || 2 * tig >= ahi) sc4[0] = sc4[2] = -INFINITY;
             if (2 * tig + 1 < alo || 2 * tig + 1 >= ahi) sc4[1] = sc4[3] = -INFINITY;
+          }
+          if constexpr (CK == kScored) {
+            float* lg = a.logits + ((int64_t(cc.i) * Hkv + cc.g) * ctx_cap + cc.p * kBS) * G + 2 * tig;
+            *reinterpret_cast<float2*>(lg + gr * G) = make_float2(sc4[0], sc4[1]);
+            *reinterpret_cast<float2*>(lg + (gr + 8) * G) = make_float2(sc4[2], sc4[3]);
           }
           float pm0 = fmaxf(sc4[0], sc4[2]), pm1 = fmaxf(sc4[1], sc4[3]);
 #pragma unroll
@@ -1062,6 +1079,20 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
         for (int jj = 0; jj < GH; ++jj) {
           const int j = (G >= 2 && hi_half) ? jj + GH : jj;
           if (j < alo || j >= ahi) sc[jj] = -INFINITY;
+        }
+      }
+
+      if constexpr (CK == kScored) {
+        // this lane's (token, heads): G / 2 neighbouring heads (G = 1: even lanes)
+        float* lg = a.logits + ((int64_t(cc.i) * Hkv + cc.g) * ctx_cap + cc.p * kBS + t_own) * G + (hi_half ? GH : 0);
+        if constexpr (G == 1) {
+          if (!hi_half) lg[0] = sc[0];
+        } else if constexpr (GH == 1) {
+          lg[0] = sc[0];
+        } else if constexpr (GH == 2) {
+          *reinterpret_cast<float2*>(lg) = make_float2(sc[0], sc[1]);
+        } else {
+          *reinterpret_cast<float4*>(lg) = make_float4(sc[0], sc[1], sc[2], sc[3]);
         }
       }
 
@@ -1234,7 +1265,7 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
         const bool row_unit = unp == cc.np;
         const bool whole_unit = seg_p0 == up0 && cc.p == up0 + unp - 1;
         if (whole_unit && row_unit) {
-          for_owned([&](int j, int ch, const float* f, float, float l, bool) {
+          for_owned([&](int j, int ch, const float* f, float mj, float l, bool lse_lane) {
             // query row j -> (sequence, head); a group row's rows past its
             // last member are dropped, and a member that attended nothing
             // (no context) gets a zero row
@@ -1244,6 +1275,8 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
               seq = cg.s0 + j / a.g_real;
               head = cc.g * a.g_real + j % a.g_real;
             }
+            if constexpr (CK == kScored)
+              if (lse_lane) a.lse2[int64_t(seq) * H + head] = mj + log2f(l);
             const float inv = (CK != kGroup || l > 0.f) ? vscale / l : 0.f;
             float y[EPV];
 #pragma unroll
@@ -1309,6 +1342,8 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
                   seq = cg.s0 + j / a.g_real;
                   head = cc.g * a.g_real + j % a.g_real;
                 }
+                if constexpr (CK == kScored)
+                  if (lane == 0) a.lse2[int64_t(seq) * H + head] = lse_m[j] * 1.4426950408889634f;
                 store_out_small<Tq, PER>(
                     reinterpret_cast<Tq*>(a.out) + int64_t(seq) * a.o_sb + int64_t(head) * a.o_sh + lane * PER, acc[j]);
               }

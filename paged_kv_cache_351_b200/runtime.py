@@ -15,8 +15,10 @@ from typing import Optional, Sequence, Tuple
 import numpy as np
 import torch
 
-from . import (Allocator, pa_copy_blocks, pa_decode, pa_decode_cascade, pa_decode_cascade_workspace_bytes,
-               pa_decode_fp8, pa_decode_workspace_bytes, pa_reshape_and_cache, pa_reshape_and_cache_fp8,
+from . import (Allocator, pa_copy_blocks, pa_decode, pa_decode_cascade,
+               pa_decode_cascade_workspace_bytes, pa_decode_fp8, pa_decode_scored, pa_decode_scored_workspace_bytes,
+               pa_decode_workspace_bytes, pa_evict, pa_reshape_and_cache, pa_reshape_and_cache_fp8,
+               pa_tree_attention, pa_tree_attention_workspace_bytes, pa_tree_commit,
                prepare_decode, prepare_decode_cascade, prepare_decode_fp8, prepare_reshape_and_cache,
                prepare_reshape_and_cache_fp8)
 
@@ -39,6 +41,8 @@ class PagedKVCacheGPU:
         self.alloc = Allocator(num_blocks, block_size, free_order)
         self._ws = None
         self._cws = None
+        self._tws = None
+        self._sws = None
         self.k_scale = self.v_scale = None
         if dtype == "fp8":
             if k_scale is None or v_scale is None:
@@ -55,6 +59,10 @@ class PagedKVCacheGPU:
 
     def free(self, seq: int) -> None:
         self.alloc.free(seq)
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Give back the slots of a sequence's rejected drafted tokens."""
+        self.alloc.truncate(seq, new_len)
 
     def append(self, seqs: Sequence[int], counts: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
         """Reserve slots for counts[k] new tokens of seqs[k]; returns (slots
@@ -143,6 +151,80 @@ class PagedKVCacheGPU:
             pa_decode(out, query, self.k_cache, self.v_cache, block_tables, context_lens, scale, self.num_kv_heads,
                       workspace=workspace, partition_tokens=partition_tokens, stream=stream)
         return out
+
+    # -- speculative decoding ---------------------------------------------------------
+    def tree_attention(self, out: torch.Tensor, query: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, query_start: torch.Tensor, tree_mask: torch.Tensor,
+                       max_query_len: int, scale: float, stream=None, workspace=None) -> torch.Tensor:
+        """Attention of every sequence's drafted tokens over its cache
+        (pa_tree_attention; the drafted tokens are already written).  The
+        workspace kept here serves one stream."""
+        if workspace is None:
+            n = pa_tree_attention_workspace_bytes(query.shape[1], self.num_kv_heads, self.head_size, max_query_len)
+            if self._tws is None or self._tws.numel() < n:
+                self._tws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            workspace = self._tws
+        pa_tree_attention(out, query, self.k_cache, self.v_cache, block_tables, context_lens, query_start, tree_mask,
+                          max_query_len, scale, self.num_kv_heads, workspace=workspace, stream=stream)
+        return out
+
+    def tree_commit(self, block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                    accepted: torch.Tensor, num_accepted: torch.Tensor, stream=None) -> None:
+        """Move the accepted drafted tokens' K/V behind the context
+        (pa_tree_commit); ``truncate`` then drops the rest of the draft."""
+        pa_tree_commit(self.k_cache, self.v_cache, block_tables, context_lens, query_start, accepted, num_accepted,
+                       stream=stream)
+
+    # -- bounded caches -----------------------------------------------------------------
+    def decode_scored(self, out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
+                      block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                      partition_tokens: int = 0, stream=None, workspace=None) -> torch.Tensor:
+        """decode, with every cached token's attention weight added to
+        ``scores`` [B, num_kv_heads, S] (pa_decode_scored)."""
+        if workspace is None:
+            n = pa_decode_scored_workspace_bytes(query.shape[0], query.shape[1], self.num_kv_heads, self.head_size,
+                                                 block_tables.shape[1], partition_tokens)
+            if self._sws is None or self._sws.numel() < n:
+                self._sws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            workspace = self._sws
+        pa_decode_scored(out, scores, query, self.k_cache, self.v_cache, block_tables, context_lens, scale,
+                         self.num_kv_heads, workspace, k_scale=self.k_scale, v_scale=self.v_scale,
+                         partition_tokens=partition_tokens, stream=stream)
+        return out
+
+    def evict(self, seqs: Sequence[int], keep: Sequence[int], scores: torch.Tensor, scores_out: torch.Tensor,
+              num_sink: int = 0, num_recent: int = 0, stream=None) -> torch.Tensor:
+        """Shorten sequences to ``keep[k]`` tokens each by accumulated weight
+        (row k of ``scores``; pa_evict): the allocator gives them fresh
+        blocks, the kept tokens move there, and ``scores_out`` gets their
+        scores.  Returns the kept positions, int32 [n, num_kv_heads, *].
+        Raises OutOfBlocksError, with nothing changed, when the fresh blocks
+        do not all fit beside the old ones."""
+        lens = [self.alloc.length(s) for s in seqs]
+        new = [min(int(k), n) for k, n in zip(keep, lens)]
+        if len(keep) != len(seqs) or min(new, default=0) < 0 or num_sink < 0 or num_recent < 0:
+            raise ValueError("one length >= 0 per sequence, num_sink and num_recent >= 0")
+        # everything pa_evict would refuse, before the allocator changes
+        for t, need, what in ((scores, max(lens, default=0), "scores"), (scores_out, max(new, default=0), "scores_out")):
+            if (tuple(t.shape[:2]) != (len(new), self.num_kv_heads) or t.dim() != 3 or t.shape[2] < need or
+                    t.dtype != torch.float32 or t.device != self.k_cache.device or t.stride(2) != 1 or
+                    t.stride(1) < t.shape[2] or t.stride(0) < t.shape[2]):
+                raise ValueError(f"{what} must be float32 [{len(new)}, {self.num_kv_heads}, at least {need}] on "
+                                 f"{self.k_cache.device} with contiguous rows")
+        if scores.numel() and scores.data_ptr() == scores_out.data_ptr():
+            raise ValueError("scores_out must not be scores")
+        bs = self.block_size
+        src, ctx = self.alloc.block_tables(seqs, max([(n + bs - 1) // bs for n in lens] + [1]))
+        dst = self.alloc.compact(seqs, new, max([(n + bs - 1) // bs for n in new] + [1]))
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        # the uploads belong to the stream that reads them
+        with torch.cuda.stream(stream):
+            kept = torch.empty(len(new), self.num_kv_heads, max(new, default=0), dtype=torch.int32, device=self.device)
+            up = [torch.from_numpy(x).to(self.device) for x in (src, ctx, dst, np.asarray(new, np.int32))]
+            pa_evict(self.k_cache, self.v_cache, up[0], up[1], scores, up[2], up[3], num_sink, num_recent, scores_out,
+                     kept, stream=stream)
+        return kept
 
     def prepare_step(self, slots: torch.Tensor, key: torch.Tensor, value: torch.Tensor, out: torch.Tensor,
                      query: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
