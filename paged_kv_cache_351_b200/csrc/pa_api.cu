@@ -20,6 +20,7 @@
 #include "pa_decode.cuh"
 #include "pa_prefill.cuh"
 #include "pa_tree.cuh"
+#include "pa_tree_mma.cuh"
 #include "pa_evict.cuh"
 
 namespace {
@@ -1005,24 +1006,44 @@ pa_status check_rows2(const pa_tensor* t, int32_t dtype, int64_t n) {
 }
 
 // Launch shape of a tree attention: R query rows per unit, KT keys per tile,
-// worker CTAs, and the warps that count shares in.
+// worker CTAs, and counters per worker.  bf16 caches run on the tensor
+// cores, in one half of 128 rows while every sequence's rows per kv head fit
+// it, else in two (see pa_tree_mma.cuh).
 struct TreePlan {
-  int R, KT, workers, warps;
+  int R, KT, workers, counters, halves;  // halves 0: the CUDA-core kernel
 };
 
 constexpr int kTreeSimtCtas = 4;  // CTAs per SM of the CUDA-core kernel (its shared memory allows 5)
 
-pa_status tree_plan(TreePlan* p) {
+pa_status tree_plan(int32_t dt, int64_t rows, TreePlan* p) {
   DeviceInfo di;
   const pa_status st = device_info(&di, nullptr);
   if (st != PA_OK) return st;
-  *p = TreePlan{pa::kTsRows, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps};
+  if (dt != PA_BF16)
+    *p = TreePlan{pa::kTsRows, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps, 0};
+  else if (rows <= 128)
+    *p = TreePlan{128, pa::TreeMma<128, 1>::KT, di.sms * pa::TreeMma<128, 1>::CTAS, 4, 1};
+  else
+    *p = TreePlan{256, pa::TreeMma<128, 2>::KT, di.sms * pa::TreeMma<128, 2>::CTAS, 8, 2};
+  if (int64_t(p->workers) * p->counters > kMaxWorkers) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
 // Header, shares (two slots per worker), their (max, denominator) pairs.
 size_t tree_ws_bytes(const TreePlan& p, int64_t D) {
   return kWsHeader + align_up(size_t(2) * p.workers * p.R * D * 4, 256) + align_up(size_t(2) * p.workers * p.R * 8, 256);
+}
+
+template <int D, int HALVES>
+pa_status run_tree_mma(const pa::TreeArgs& a, const TreePlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                       const CUtensorMap& tv, cudaStream_t s, int dev) {
+  static std::atomic<size_t> smem_limit[kMaxDevices];
+  using C = pa::TreeMma<D, HALVES>;
+  auto kern = pa::tree_mma_kernel<D, HALVES>;
+  if (!raise_smem_limit(kern, size_t(C::SMEM), dev, smem_limit)) return PA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(unsigned(p.workers)), dim3(C::THREADS), C::SMEM, s, true, tq, tk, tv, a) != cudaSuccess)
+    return launch_status();
+  return PA_OK;
 }
 
 template <typename T, int D>
@@ -1046,10 +1067,13 @@ pa_status pa_tree_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_he
       max_query_len < 0)
     return PA_ERR_INVALID_ARG;
   *bytes_out = 0;
-  TreePlan p;
-  const pa_status st = tree_plan(&p);
-  if (st != PA_OK) return st;
-  *bytes_out = tree_ws_bytes(p, head_size);
+  const int64_t rows = int64_t(max_query_len) * (num_heads / num_kv_heads);
+  for (int32_t dt : {PA_F32, PA_BF16}) {
+    TreePlan p;
+    const pa_status st = tree_plan(dt, rows, &p);
+    if (st != PA_OK) return st;
+    *bytes_out = std::max(*bytes_out, tree_ws_bytes(p, head_size));
+  }
   return PA_OK;
 }
 
@@ -1091,7 +1115,7 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (B == 0 || T == 0) return PA_OK;
 
   TreePlan p;
-  if ((st = tree_plan(&p)) != PA_OK) return st;
+  if ((st = tree_plan(dt, max_query_len * G, &p)) != PA_OK) return st;
   // the tile list is indexed with 32 bits
   const int64_t tiles_max = B * Hkv * ((max_query_len * G + p.R - 1) / p.R) * ((max_nb * 16 + p.KT - 1) / p.KT);
   if (tiles_max > INT32_MAX) return PA_ERR_UNSUPPORTED;
@@ -1125,11 +1149,29 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
   cudaStream_t s = stream_of(opts);
-  if (dt == PA_BF16 && D == 128) return run_tree_simt<__nv_bfloat16, 128>(a, p, s, dev);
-  if (dt == PA_BF16 && D == 64) return run_tree_simt<__nv_bfloat16, 64>(a, p, s, dev);
-  if (dt == PA_F32 && D == 128) return run_tree_simt<float, 128>(a, p, s, dev);
-  if (dt == PA_F32 && D == 64) return run_tree_simt<float, 64>(a, p, s, dev);
-  return PA_ERR_UNSUPPORTED;
+  if (dt == PA_F32) return D == 128 ? run_tree_simt<float, 128>(a, p, s, dev) : run_tree_simt<float, 64>(a, p, s, dev);
+
+  DeviceInfo di;
+  if ((st = device_info(&di, nullptr)) != PA_OK) return st;
+  if (di.smem_optin < int(pa::TreeMma<128, 2>::SMEM)) return PA_ERR_UNSUPPORTED;
+  CUtensorMap tq, tk, tv;
+  {
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
+    const cuuint64_t strides[2] = {cuuint64_t(query->stride[1]) * 2, cuuint64_t(query->stride[0]) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(128 / G)};
+    if ((st = bf16_map(&tq, query->data, 3, dims, strides, box)) != PA_OK) return st;
+  }
+  {
+    const cuuint64_t dims[4] = {cuuint64_t(D), 16, cuuint64_t(Hkv), cuuint64_t(NB)};
+    const cuuint64_t strides[3] = {cuuint64_t(D) * 2, cuuint64_t(16 * D) * 2, cuuint64_t(Hkv * 16 * D) * 2};
+    const cuuint32_t box[4] = {64, 16, 1, 1};
+    if ((st = bf16_map(&tk, k_cache->data, 4, dims, strides, box)) != PA_OK) return st;
+    if ((st = bf16_map(&tv, v_cache->data, 4, dims, strides, box)) != PA_OK) return st;
+  }
+  if (D == 128)
+    return p.halves == 1 ? run_tree_mma<128, 1>(a, p, tq, tk, tv, s, dev)
+                         : run_tree_mma<128, 2>(a, p, tq, tk, tv, s, dev);
+  return p.halves == 1 ? run_tree_mma<64, 1>(a, p, tq, tk, tv, s, dev) : run_tree_mma<64, 2>(a, p, tq, tk, tv, s, dev);
 }
 
 pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
