@@ -1022,9 +1022,9 @@ pa_status tree_plan(int32_t dt, int64_t rows, TreePlan* p) {
   if (dt != PA_BF16)
     *p = TreePlan{pa::kTsRows, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps, 0};
   else if (rows <= 128)
-    *p = TreePlan{128, pa::TreeMma<128, 1>::KT, di.sms * pa::TreeMma<128, 1>::CTAS, 4, 1};
+    *p = TreePlan{128, pa::TreeMma<128, 1>::KT, di.sms * pa::TreeMma<128, 1>::CTAS, 1, 1};
   else
-    *p = TreePlan{256, pa::TreeMma<128, 2>::KT, di.sms * pa::TreeMma<128, 2>::CTAS, 8, 2};
+    *p = TreePlan{256, pa::TreeMma<128, 2>::KT, di.sms * pa::TreeMma<128, 2>::CTAS, 2, 2};
   if (int64_t(p->workers) * p->counters > kMaxWorkers) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
@@ -1116,8 +1116,8 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
 
   TreePlan p;
   if ((st = tree_plan(dt, max_query_len * G, &p)) != PA_OK) return st;
-  // the tile list is indexed with 32 bits
-  const int64_t tiles_max = B * Hkv * ((max_query_len * G + p.R - 1) / p.R) * ((max_nb * 16 + p.KT - 1) / p.KT);
+  // the list of units (tiles and lead) is indexed with 32 bits
+  const int64_t tiles_max = B * Hkv * ((max_query_len * G + p.R - 1) / p.R) * ((max_nb * 16 + p.KT - 1) / p.KT + 8);
   if (tiles_max > INT32_MAX) return PA_ERR_UNSUPPORTED;
   pa::TreeArgs a;
   std::memset(&a, 0, sizeof(a));

@@ -12,11 +12,12 @@
 // query rows), the rows being the unit's drafted tokens times the G query
 // heads of the kv head, so that a K/V page is read once for all of them; it
 // is a run of key tiles of KT tokens.  The workers (CTAs) of a persistent
-// grid take equal contiguous ranges of the flattened tile list, whatever the
-// mix of lengths; a unit cut by a range boundary leaves one share per worker
-// (output before the division, running max, denominator), and the warp that
-// counts in the unit's last tiles merges the shares of its rows in worker
-// order.  Nobody waits for anybody, the result does not depend on who came
+// grid take equal contiguous ranges of the flattened list of units, whatever
+// the mix of lengths; a unit counts as its tiles plus LEAD (what a unit costs
+// beside its tiles, in tiles), which stand before its first tile and hold no
+// work.  A unit cut by a range boundary leaves one share per worker
+// (output before the division, running max, denominator), and whoever counts
+// in the unit's last tiles merges the shares in worker order.  Nobody waits for anybody, the result does not depend on who came
 // last, and every counter is zero again when the launch ends.
 #pragma once
 
@@ -40,7 +41,7 @@ struct TreeArgs {
   int32_t split;     // 1: units may be cut between workers (shares below)
   float* sh_o;       // shares: two slots per worker, [R][D] floats each
   float2* sh_ml;     // [R] (running max in log2 units, denominator)
-  unsigned int* cnt; // per worker and warp: tiles of the unit that starts there counted in so far
+  unsigned int* cnt; // per worker and warp (or half): tiles of the unit that starts there counted in so far
   uint64_t timeout_ns;
 };
 
@@ -60,13 +61,28 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int i) {
   return TreeSeq{int(q0), int(n), ctx - int(n)};
 }
 
-// Position in the flattened tile list: sequence, unit of the sequence (kv
-// head major, row tile minor), key tile of the unit.
+// Position in the flattened list: sequence, unit of the sequence (kv head
+// major, row tile minor), position in the unit (LEAD, then its key tiles).
 struct TreePos {
   int i, u, p;
   int units, nt;  // units of the sequence, key tiles of each
   TreeSeq s;
 };
+
+// A worker's part of one unit: key tiles [b, e) (none if the part lies in the
+// lead), and where the part ends in the unit's list.
+struct TreeSeg {
+  int b, e, pe;
+};
+
+template <int LEAD>
+__device__ __forceinline__ TreeSeg tree_seg(const TreePos& x, int left) {
+  TreeSeg g;
+  g.pe = x.nt + LEAD - x.p < left ? x.nt + LEAD : x.p + left;
+  g.b = max(0, x.p - LEAD);
+  g.e = max(0, g.pe - LEAD);
+  return g;
+}
 
 template <int R, int KT>
 __device__ __forceinline__ void tree_shape(const TreeArgs& a, TreePos& x) {
@@ -88,14 +104,29 @@ __device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreePos& x) {
   } while (x.units == 0);
 }
 
-// Whole block: this worker's range [lo, hi) of the tile list, the list's
-// length, and the position of lo.  smem: 40 ints.
+// Whole block: this worker's range [lo, hi) of the list, the list's length, and the position of lo.  smem: 40 ints.
+//
+// Workers past N = W / MIN_LEN (at least 1, at most the grid) get nothing: a
+// short list is cut into fewer pieces, since a share costs a write and the
+// merge a read, and no worker of the others is empty.
 struct TreeRange {
-  int64_t W, lo, hi;
+  int W, N;    // length of the list, workers
+  int per, rem;  // W / N, W % N
+  int lo, hi;
   TreePos at;
+  // first position of worker w: ceil(w W / N), in 32 bits (N is at most the
+  // grid, below 2^15, so w rem + N does not overflow)
+  __device__ __forceinline__ int first(int w) const { return w * per + (w * rem + N - 1) / N; }
+  // the worker that holds position x: an estimate, then exact
+  __device__ __forceinline__ int owner(int x) const {
+    int w = min(N - 1, int(__fdividef(float(x), float(per) + __fdividef(float(rem), float(N)))));
+    while (first(w) > x) --w;
+    while (w + 1 < N && first(w + 1) <= x) ++w;
+    return w;
+  }
 };
 
-template <int R, int KT>
+template <int R, int KT, int LEAD, int MIN_LEN>
 __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   const int nthr = blockDim.x;
   const int per = (a.B + nthr - 1) / nthr;
@@ -105,32 +136,35 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
     TreePos x;
     x.i = i;
     tree_shape<R, KT>(a, x);
-    local += x.units * x.nt;
+    local += x.units > 0 ? x.units * (x.nt + LEAD) : 0;
   }
   int total;
   const int first = block_exclusive_scan(local, smem, &total);
   TreeRange r;
   r.W = total;
-  const int64_t N = gridDim.x, w = blockIdx.x;
-  r.lo = (w * r.W + N - 1) / N;
-  r.hi = ((w + 1) * r.W + N - 1) / N;
+  r.N = max(1, min(int(gridDim.x), total / MIN_LEN));
+  r.per = total / r.N;
+  r.rem = total - r.per * r.N;
+  const int w = min(int(blockIdx.x), r.N);
+  r.lo = r.first(w);
+  r.hi = w < r.N ? r.first(w + 1) : r.lo;
   // the thread that owns the tile finds its sequence; without a split both
   // ends move down to the start of their unit
   for (int e = 0; e < 2; ++e) {
-    const int64_t b = e == 0 ? r.lo : r.hi;
+    const int b = e == 0 ? r.lo : r.hi;
     if (b < r.W && b >= first && b < first + local) {
       int base = first;
       for (int i = i0; i < i1; ++i) {
         TreePos x;
         x.i = i;
         tree_shape<R, KT>(a, x);
-        const int t = x.units * x.nt;
+        const int len = x.nt + LEAD, t = x.units * len;
         if (b < base + t) {
-          const int off = int(b) - base;
+          const int off = b - base;
           smem[32 + 4 * e + 0] = i;
-          smem[32 + 4 * e + 1] = off / x.nt;
-          smem[32 + 4 * e + 2] = a.split ? off % x.nt : 0;
-          smem[32 + 4 * e + 3] = a.split ? 0 : off % x.nt;
+          smem[32 + 4 * e + 1] = off / len;
+          smem[32 + 4 * e + 2] = a.split ? off % len : 0;
+          smem[32 + 4 * e + 3] = a.split ? 0 : off % len;
           break;
         }
         base += t;
@@ -169,6 +203,14 @@ __device__ __forceinline__ uint32_t tree_seen32(const TreeArgs& a, int64_t row, 
   return (tree_word(a, row, n, 0) << k) | ((1u << k) - 1u);
 }
 
+// 1 / (a row's denominator); 0 for a row that sees nothing, whose output is zero.
+__device__ __forceinline__ float tree_inverse(const TreeArgs& a, float l, int c0, int n, int64_t row) {
+  if (l != 0.f || c0 > 0) return 1.f / l;
+  for (int w = 0; w * 32 < n; ++w)
+    if (tree_word(a, row, n, w) != 0u) return 1.f / l;
+  return 0.f;
+}
+
 // ---- CUDA-core kernel ----------------------------------------------------
 // fp32 caches: products and sums in fp32, no tensor-core rounding.  R = 16
 // query rows per CTA, four to a warp; a tile of 32 keys is staged in shared
@@ -179,6 +221,8 @@ __device__ __forceinline__ uint32_t tree_seen32(const TreeArgs& a, int64_t row, 
 constexpr int kTsRows = 16;
 constexpr int kTsKeys = 32;
 constexpr int kTsWarps = 4;
+constexpr int kTsLead = 1;
+constexpr int kTsMinLen = 2;
 
 template <int D>
 constexpr size_t tree_simt_smem() {
@@ -197,18 +241,22 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 
   pdl_wait();
   pdl_launch_dependents();
-  const TreeRange rg = tree_range<kTsRows, kTsKeys>(a, scratch);
+  const TreeRange rg = tree_range<kTsRows, kTsKeys, kTsLead, kTsMinLen>(a, scratch);
   TreePos x = rg.at;
-  const int64_t N = gridDim.x;
   const uint4* kc = static_cast<const uint4*>(a.kc);
   const uint4* vc = static_cast<const uint4*>(a.vc);
 
-  for (int64_t cx = rg.lo; cx < rg.hi;) {
-    // ---- one segment: this worker's tiles [x.p, pe) of one unit ----
+  for (int cx = rg.lo; cx < rg.hi;) {
+    // ---- one segment: this worker's tiles of one unit ----
+    const TreeSeg sg = tree_seg<kTsLead>(x, rg.hi - cx);
+    if (sg.b == sg.e) {
+      cx += sg.pe - x.p;
+      if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
+      continue;
+    }
     const int rts = x.units / a.Hkv;
     const int kvh = x.u / rts, r0 = (x.u % rts) * kTsRows;
     const int rows = min(kTsRows, x.s.n * a.G - r0);
-    const int pe = int(x.nt - x.p < rg.hi - cx ? x.nt : x.p + (rg.hi - cx));
     const int kv_len = x.s.c0 + x.s.n;
     for (int e = threadIdx.x; e < kTsRows * VPR; e += blockDim.x) {
       const int r = e / VPR, c = e % VPR;
@@ -232,7 +280,7 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 #pragma unroll
       for (int e = 0; e < PER; ++e) o[r][e] = 0.f;
     }
-    for (int p = x.p; p < pe; ++p) {
+    for (int p = sg.b; p < sg.e; ++p) {
       const int key0 = p * kTsKeys;
       __syncthreads();  // the previous tile (and the query rows) are no longer in use / are complete
       for (int e = threadIdx.x; e < kTsKeys * VPR; e += blockDim.x) {
@@ -314,43 +362,56 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int k = 16; k > 0; k >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
 
     // ---- the segment's result: rows of the output, or a share of a cut unit ----
-    const bool whole = x.p == 0 && pe == x.nt;
-    const int64_t unit0 = cx - x.p;  // the unit's first tile in the list
+    const bool whole = sg.b == 0 && sg.e == x.nt;
+    const int unit0 = cx - x.p + kTsLead;  // the unit's first tile in the list
     bool write = whole;
     if (!whole) {
-      const int64_t wa = unit0 * N / rg.W;
+      const int wa = rg.owner(unit0);
       const int64_t slot = share_slot(blockIdx.x, wa);
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
         if (warp * RW + r >= rows) continue;
         const int64_t row = slot * kTsRows + warp * RW + r;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) a.sh_o[row * D + lane * PER + e] = o[r][e];
+        for (int e = 0; e < PER; ++e) __stcg(a.sh_o + row * D + lane * PER + e, o[r][e]);
         if (lane == 0) a.sh_ml[row] = make_float2(m[r], l[r]);
       }
-      write = share_done(a.cnt + wa * kTsWarps + warp, pe - x.p, x.nt);
+      write = share_done(a.cnt + wa * kTsWarps + warp, sg.e - sg.b, x.nt);
       if (write) {
-        const int64_t wb = (unit0 + x.nt - 1) * N / rg.W;
+        // Lane t holds the (max, denominator) pair of share k0 + t and turns
+        // it into a weight; the weights are broadcast while every lane adds
+        // its dims, several shares' loads in flight.
+        const int ns = rg.owner(unit0 + x.nt - 1) - wa + 1;
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
-          m[r] = -INFINITY;
+          if (warp * RW + r >= rows) continue;
+          const int64_t row0 = warp * RW + r;
+          auto pair = [&](int k) {
+            return k < ns ? __ldcg(a.sh_ml + share_slot(wa + k, wa) * kTsRows + row0) : make_float2(-INFINITY, 0.f);
+          };
+          float mx = -INFINITY;
+          for (int k0 = 0; k0 < ns; k0 += 32) mx = fmaxf(mx, pair(k0 + lane).x);
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          const float mu = mx == -INFINITY ? 0.f : mx;
           l[r] = 0.f;
 #pragma unroll
           for (int e = 0; e < PER; ++e) o[r][e] = 0.f;
-          if (warp * RW + r >= rows) continue;
-          for (int64_t k = wa; k <= wb; ++k) {
-            if (worker_empty(k, rg.W, N)) continue;
-            const int64_t row = share_slot(k, wa) * kTsRows + warp * RW + r;
-            const float2 ml = __ldcg(a.sh_ml + row);
-            if (ml.y == 0.f) continue;  // a share that saw nothing
-            const float mn = fmaxf(m[r], ml.x);
-            const float al = ex2(m[r] - mn), be = ex2(ml.x - mn);
-            m[r] = mn;
-            l[r] = l[r] * al + ml.y * be;
+          for (int k0 = 0; k0 < ns; k0 += 32) {
+            const float2 ml = pair(k0 + lane);
+            const float wl = ex2(ml.x - mu);
+            l[r] += ml.y * wl;
+            const int nk = min(32, ns - k0);
+#pragma unroll 8
+            for (int t = 0; t < nk; ++t) {
+              const float w = __shfl_sync(0xffffffffu, wl, t);
+              const float* src = a.sh_o + (share_slot(wa + k0 + t, wa) * kTsRows + row0) * D + lane * PER;
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-              o[r][e] = o[r][e] * al + (be == 0.f ? 0.f : __ldcg(a.sh_o + row * D + lane * PER + e) * be);
+              for (int e = 0; e < PER; ++e) o[r][e] = fmaf(w, __ldcg(src + e), o[r][e]);
+            }
           }
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
         }
       }
     }
@@ -359,17 +420,17 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int r = 0; r < RW; ++r) {
         if (warp * RW + r >= rows) continue;
         const int row = r0 + warp * RW + r;
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // 0: the row sees nothing
+        const float inv = tree_inverse(a, l[r], x.s.c0, x.s.n, x.s.q0 + row / a.G);
         float y[PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) y[e] = l[r] == 0.f ? 0.f : o[r][e] * inv;
+        for (int e = 0; e < PER; ++e) y[e] = o[r][e] * inv;
         store_out_small<T, PER>(static_cast<T*>(a.out) + (x.s.q0 + row / a.G) * a.o_st +
                                     (kvh * a.G + row % a.G) * a.o_sh + lane * PER,
                                 y);
       }
     }
-    cx += pe - x.p;
-    tree_next_unit<kTsRows, kTsKeys>(a, x);
+    cx += sg.pe - x.p;
+    if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
     __syncthreads();  // the query rows are replaced by the next segment's
   }
 }

@@ -36,6 +36,11 @@ struct TreeMma {
   static constexpr int R = 128 * HALVES;
   static constexpr int KT = HALVES == 1 ? 64 : 128;
   static constexpr int NB = HALVES == 1 ? 2 : 1;  // S buffers per half
+  // A unit's cost beside its tiles, in tiles (LLaMA batch of 16-token trees,
+  // 12 tiles a unit: 0.197 ms with 0, 0.172 with 1, 0.154 with 2, 0.150 with
+  // 3), and the least list length worth a worker of its own.
+  static constexpr int LEAD = HALVES == 1 ? 3 : 1;
+  static constexpr int MIN_LEN = 4;
   static constexpr int NH = D / 64;               // 64-dim halves of the head dimension
   static constexpr int THREADS = 128 + HALVES * 128;
   static constexpr int CTAS = HALVES == 1 ? 2 : 1;  // per SM
@@ -75,12 +80,16 @@ enum TmBar : int {
   kTmDrain = 24,
   kTmBDone = 25,  // half B's warps have read a unit's results, 4 arrivals
   kTmSlot = 26,   // 4-byte TMEM base address
+  kTmLast = 27,   // + half * 4 bytes: this half completes a cut unit
 };
 
 // bf16 pair: a mask of the halves (low 0xffff, high 0xffff0000) that are infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
+
+// The four softmax warps of one half.
+__device__ __forceinline__ void half_sync(int hx) { asm volatile("bar.sync %0, 128;" ::"r"(1 + hx) : "memory"); }
 
 template <int D, int HALVES>
 __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES>::CTAS)
@@ -107,32 +116,43 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     mbar_init(bar(kTmDrain), 1);
     mbar_init(bar(kTmBDone), 4);
     fence_barrier_init();
+    tc::tma_prefetch_desc(&tm_q);
+    tc::tma_prefetch_desc(&tm_k);
+    tc::tma_prefetch_desc(&tm_v);
   }
   pdl_wait();
   pdl_launch_dependents();
-  const TreeRange rg = tree_range<R, KT>(a, reinterpret_cast<int*>(gbase + C::SCAN));
+  const TreeRange rg = tree_range<R, KT, C::LEAD, C::MIN_LEN>(a, reinterpret_cast<int*>(gbase + C::SCAN));
   if (rg.lo >= rg.hi) return;  // the whole CTA: nothing allocated or in flight
   if (warp == 1) tc::tmem_alloc(bar(kTmSlot), C::TCOLS);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::BAR + 8 * kTmSlot);
-  const int64_t N = gridDim.x;
 
-  // Every role walks the same segments: this worker's tiles [x.p, pe) of one
+  // Every role walks the same segments: this worker's key tiles [b, e) of one
   // unit after another.  t counts tiles, seg segments.
   TreePos x = rg.at;
-  int64_t cx = rg.lo;
-  auto seg_end = [&]() { return int(x.nt - x.p < rg.hi - cx ? x.nt : x.p + (rg.hi - cx)); };
+  int cx = rg.lo;
+  TreeSeg sg{0, 0, 0};
   auto unit_rows = [&](int& kvh, int& r0) {  // kv head, first row and rows of the unit
     const int rts = x.units / a.Hkv;
     kvh = x.u / rts;
     r0 = (x.u - kvh * rts) * R;
     return min(R, x.s.n * a.G - r0);
   };
-  auto advance = [&](int pe) {
-    cx += pe - x.p;
+  auto advance = [&]() {
+    cx += sg.pe - x.p;
     if (cx < rg.hi) tree_next_unit<R, KT>(a, x);
+  };
+  // the segment at cx, past parts that hold no tile; false at the end
+  auto next_seg = [&]() {
+    while (cx < rg.hi) {
+      sg = tree_seg<C::LEAD>(x, rg.hi - cx);
+      if (sg.b < sg.e) return true;
+      advance();
+    }
+    return false;
   };
 
   if (warp == 0 || warp == 2) {
@@ -142,17 +162,15 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
     const uint32_t ring = base + (is_k ? C::K0 : C::V0);
     const int full0 = is_k ? kTmKFull : kTmVFull, free0 = is_k ? kTmKFree : kTmVFree;
-    if (lane == 0) tc::tma_prefetch_desc(tm);
     int t = 0;
     bool ok = true;
-    while (ok && cx < rg.hi) {
+    while (ok && next_seg()) {
       int kvh, r0;
       unit_rows(kvh, r0);
-      const int pe = seg_end();
       const int npages = (x.s.c0 + x.s.n + kBS - 1) / kBS;
       const int32_t* bt = a.bt + int64_t(x.i) * a.bt_stride;
       int win = -1, ids = 0;  // 32 block ids of the table from page `win` on, one per lane
-      for (int p = x.p; p < pe; ++p, ++t) {
+      for (int p = sg.b; p < sg.e; ++p, ++t) {
         const int st = t % nst;
         const int p0 = p * (KT / kBS), np = min(KT / kBS, npages - p0);
         if (win < 0 || p0 + KT / kBS > win + 32) {
@@ -175,16 +193,15 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
           }
         }
       }
-      advance(pe);
+      advance();
     }
     // before the CTA may exit, every copy it started must have landed
     for (int j = max(0, t - nst); j < t; ++j) mbar_wait_bounded(bar(full0 + j % nst), (j / nst) & 1, a.timeout_ns);
   } else if (warp == 3) {
     // ---------------- Q producer ----------------
-    if (lane == 0) tc::tma_prefetch_desc(&tm_q);
     int seg = 0;
     bool ok = true;
-    while (ok && cx < rg.hi) {
+    while (ok && next_seg()) {
       int kvh, r0;
       unit_rows(kvh, r0);
       if (seg > 0 && !(ok = warp_wait(bar(kTmQFree), (seg - 1) & 1, a.timeout_ns))) break;
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
                           x.s.q0 + (r0 + (e / C::NH) * 128) / a.G, bar(kTmQFull));
       }
       ++seg;
-      advance(seg_end());
+      advance();
     }
     if (seg > 0) mbar_wait_bounded(bar(kTmQFull), (seg - 1) & 1, a.timeout_ns);
   } else if (warp == 1) {
@@ -224,10 +241,10 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     };
     int t = 0, seg = 0;
     bool ok = true;
-    while (ok && cx < rg.hi) {
+    while (ok && next_seg()) {
       int kvh, r0;
       const bool has_b = HALVES == 2 && unit_rows(kvh, r0) > 128;
-      const int pe = seg_end(), nt = pe - x.p;
+      const int nt = sg.e - sg.b;
       // Q K^T of the segment's tile j, both halves or one, then the stage is free
       auto issue_qk = [&](int j, int hx, bool last_half) {
         if (lane == 0) {
@@ -294,7 +311,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       }
       t += nt;
       ++seg;
-      advance(pe);
+      advance();
     }
     // no product may still run when TMEM is released
     if (lane == 0) tc::commit(bar(kTmDrain));
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     int cnt = 0, t = 0, seg = 0;  // tiles of this half, tiles, segments
     int seg_b = 0;                // segments with a half B before this one
     bool ok = true, prev_b = false;
-    for (; cx < rg.hi; ++seg) {
+    for (; next_seg(); ++seg) {
       int kvh, r0;
       const int rows = unit_rows(kvh, r0);
       if (HALVES == 2) {
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
         prev_b = rows > 128;
         seg_b += prev_b;
       }
-      const int pe = seg_end(), nt = pe - x.p;
+      const int nt = sg.e - sg.b;
       const int c0 = x.s.c0, n = x.s.n, kv_len = c0 + n;
       const int urow = r0 + hx * 128 + rr;  // row of the sequence's (token, head) list
       const bool row_valid = hx * 128 + rr < rows;
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       float m_used = -INFINITY, l = 0.f;
       if (hx == 0 || rows > 128) {
         for (int j = 0; ok && j < nt; ++j, ++cnt) {
-          const int key0 = (x.p + j) * KT;
+          const int key0 = (sg.b + j) * KT;
           const bool tree = key0 + KT > c0;  // drafted keys, or none, at the tile's end
           if (tree && hx == 0) {
             // Sanitise V: rows past the last key hold anything and drafted
@@ -367,7 +384,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
               for (int q = 0; q < RPI; ++q)
                 if ((vote >> (q * CPR)) & (CPR == 16 ? 0xFFFFu : 0xFFu)) bad |= 1u << (k * RPI + q);
             }
-            if (lane == 0) nonfin[((seg & 3) * C::MAXT + (x.p + j - c0 / KT)) * 4 + quad] = bad;
+            if (lane == 0) nonfin[((seg & 3) * C::MAXT + (sg.b + j - c0 / KT)) * 4 + quad] = bad;
             tc::fence_proxy_async_smem();
             __syncwarp();
           }
@@ -451,24 +468,24 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
         if (ok) ok = warp_wait(bar(kTmODone + hx), (cnt - 1) & 1, a.timeout_ns);
       }
       t += nt;
+      const bool whole = nt == x.nt;
+      const int unit0 = cx - x.p + C::LEAD;  // the unit's first tile in the list
+      const int wa = whole ? 0 : rg.owner(unit0);
       if (live) {
-        const bool whole = x.p == 0 && pe == x.nt;
-        const int64_t unit0 = cx - x.p;  // the unit's first tile in the list
-        const int64_t wa = whole ? 0 : unit0 * N / rg.W;
         // this row's share of a worker: float4 of dims 4 d .. 4 d + 3 at [d][row]
         auto share_o = [&](int64_t slot, int d4) {
           return reinterpret_cast<float4*>(a.sh_o) + ((slot * HALVES + hx) * (D / 4) + d4) * 128 + rr;
         };
         auto share_ml = [&](int64_t slot) { return a.sh_ml + (slot * HALVES + hx) * 128 + rr; };
         // drafted tokens with infinite or NaN elements of V, in the segment's tiles
-        const int tf = max(x.p, c0 / KT);
+        const int tf = max(sg.b, c0 / KT);
         uint32_t any = 0;
-        for (int p = tf; ok && p < pe; ++p)
+        for (int p = tf; ok && p < sg.e; ++p)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             any |= reinterpret_cast<volatile uint32_t*>(nonfin)[((seg & 3) * C::MAXT + (p - c0 / KT)) * 4 + q];
         auto add_nonfinite = [&](float* o, int d0) {
-          for (int p = tf; p < pe; ++p)
+          for (int p = tf; p < sg.e; ++p)
             for (int q = 0; q < 4; ++q) {
               uint32_t w = reinterpret_cast<volatile uint32_t*>(nonfin)[((seg & 3) * C::MAXT + (p - c0 / KT)) * 4 + q];
               for (; w != 0u; w &= w - 1u) {
@@ -500,77 +517,117 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
             *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = w;
           }
         };
-        // 1 / l; a row that sees nothing is zero
-        auto inverse = [&](float den) {
-          if (den != 0.f || c0 > 0) return 1.f / den;
-          for (int w = 0; w * 32 < n; ++w)
-            if (row_valid && tree_word(a, mrow, n, w) != 0u) return 1.f / den;
-          return 0.f;
-        };
         if (ok) {
           tc::fence_after_sync();
           const int64_t slot = share_slot(blockIdx.x, wa);
-          const float inv = whole ? inverse(l) : 1.f;
+          const float inv = whole ? tree_inverse(a, l, c0, n, mrow) : 1.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
+          for (int c = 0; c < D / 64; ++c) {
+            float o[64];
             __syncwarp();
-            tc::tmem_ld32(tO + uint32_t(c) * 32u, o);
-            if (any != 0u) add_nonfinite(o, c * 32);
+            tc::tmem_ld64(tO + uint32_t(c) * 64u, o);
+            if (any != 0u) {
+              add_nonfinite(o, c * 64);
+              add_nonfinite(o + 32, c * 64 + 32);
+            }
             if (whole) {
-              write_row(c, o, inv);
+              write_row(2 * c, o, inv);
+              write_row(2 * c + 1, o + 32, inv);
             } else {
 #pragma unroll
-              for (int d = 0; d < 8; ++d)
-                *share_o(slot, c * 8 + d) = make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
+              for (int d = 0; d < 16; ++d)
+                __stcg(share_o(slot, c * 16 + d), make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]));
             }
           }
           if (HALVES == 2 && hx == 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kTmBDone));
           }
-          if (!whole) *share_ml(slot) = make_float2(m_used == -INFINITY ? -INFINITY : m_used * cl, l);
-        }
-        // a cut unit: count the tiles in (after a timeout too, so that the
-        // counters end at zero); the last warp to do so merges its rows
-        if (!whole && share_done(a.cnt + (wa * HALVES + hx) * 4 + quad, nt, x.nt) && ok) {
-          const int64_t wb = (unit0 + x.nt - 1) * N / rg.W;
-          float M = -INFINITY, L = 0.f;
-          for (int64_t k = wa; k <= wb; ++k)
-            if (!worker_empty(k, rg.W, N)) M = fmaxf(M, __ldcg(share_ml(share_slot(k, wa))).x);
-          const float Mu = M == -INFINITY ? 0.f : M;
-          for (int64_t k = wa; k <= wb; ++k)
-            if (!worker_empty(k, rg.W, N)) {
-              const float2 ml = __ldcg(share_ml(share_slot(k, wa)));
-              L += ml.y * ex2(ml.x - Mu);
-            }
-          const float inv = inverse(L);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll 1
-            for (int64_t k = wa; k <= wb; ++k) {
-              if (worker_empty(k, rg.W, N)) continue;
-              const int64_t ks = share_slot(k, wa);
-              const float w = ex2(__ldcg(share_ml(ks)).x - Mu);
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                const float4 v = __ldcg(share_o(ks, c * 8 + d));
-                o[4 * d] = fmaf(w, v.x, o[4 * d]);
-                o[4 * d + 1] = fmaf(w, v.y, o[4 * d + 1]);
-                o[4 * d + 2] = fmaf(w, v.z, o[4 * d + 2]);
-                o[4 * d + 3] = fmaf(w, v.w, o[4 * d + 3]);
-              }
-            }
-            write_row(c, o, inv);
-          }
+          if (!whole) __stcg(share_ml(slot), make_float2(m_used == -INFINITY ? -INFINITY : m_used * cl, l));
         }
       } else if (HALVES == 2 && hx == 1 && rows > 128) {
         if (lane == 0) mbar_arrive(bar(kTmBDone));
       }
-      advance(pe);
+      if (!whole && rows > hx * 128) {
+        // A cut unit: the half's tiles are counted in (after a timeout too,
+        // so that the counters end at zero), and the half that completes the
+        // unit merges the shares of its rows, its four warps taking turns at
+        // pieces of 32 rows x 16 dims.  The barriers are reached by all four
+        // warps whatever happened to them.
+        half_sync(hx);
+        int* const last = reinterpret_cast<int*>(gbase + C::BAR + 8 * kTmLast) + hx;
+        if (quad == 0 && lane == 0)
+          *reinterpret_cast<volatile int*>(last) = count_in(a.cnt + wa * HALVES + hx, unsigned(nt), unsigned(x.nt));
+        half_sync(hx);
+        if (*reinterpret_cast<volatile int*>(last) && ok) {
+          const int ns = rg.owner(unit0 + x.nt - 1) - wa + 1;
+          const int pieces = (min(128, rows - hx * 128) + 31) / 32 * (D / 16);
+          for (int it = quad; it < pieces; it += 4) {
+            const int d0 = it % (D / 16) * 16, r = it / (D / 16) * 32 + lane;
+            auto slot_of = [&](int k) { return share_slot(wa + k, wa) * HALVES + hx; };
+            auto pair = [&](int k) {
+              return k < ns ? __ldcg(a.sh_ml + slot_of(k) * 128 + r) : make_float2(-INFINITY, 0.f);
+            };
+            float M = -INFINITY, L = 0.f;
+            for (int k0 = 0; k0 < ns; k0 += 8) {
+              float2 ml[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) ml[k] = pair(k0 + k);
+              float mn = M;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
+              const float mu = mn == -INFINITY ? 0.f : mn;
+              L *= ex2(M - mu);
+              M = mn;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) L += ml[k].y * ex2(ml[k].x - mu);
+            }
+            const float mu = M == -INFINITY ? 0.f : M;
+            float o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 1
+            for (int k0 = 0; k0 < ns; k0 += 4) {
+              float2 ml[4];
+              float4 v[4][4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                ml[k] = pair(k0 + k);
+                const float4* src = reinterpret_cast<const float4*>(a.sh_o) +
+                                    (slot_of(min(k0 + k, ns - 1)) * (D / 4) + d0 / 4) * 128 + r;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) v[k][d] = __ldcg(src + d * 128);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= ns) break;
+                const float w = ex2(ml[k].x - mu);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                  o[4 * d] = fmaf(w, v[k][d].x, o[4 * d]);
+                  o[4 * d + 1] = fmaf(w, v[k][d].y, o[4 * d + 1]);
+                  o[4 * d + 2] = fmaf(w, v[k][d].z, o[4 * d + 2]);
+                  o[4 * d + 3] = fmaf(w, v[k][d].w, o[4 * d + 3]);
+                }
+              }
+            }
+            if (hx * 128 + r < rows) {
+              const int row = r0 + hx * 128 + r, tk = row / a.G;
+              const float inv = tree_inverse(a, L, c0, n, x.s.q0 + tk);
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (x.s.q0 + tk) * a.o_st +
+                                   (kvh * a.G + row - tk * a.G) * a.o_sh + d0;
+#pragma unroll
+              for (int v8 = 0; v8 < 2; ++v8)
+                reinterpret_cast<uint4*>(dst)[v8] =
+                    make_uint4(pack_bf16x2(o[8 * v8] * inv, o[8 * v8 + 1] * inv),
+                               pack_bf16x2(o[8 * v8 + 2] * inv, o[8 * v8 + 3] * inv),
+                               pack_bf16x2(o[8 * v8 + 4] * inv, o[8 * v8 + 5] * inv),
+                               pack_bf16x2(o[8 * v8 + 6] * inv, o[8 * v8 + 7] * inv));
+            }
+          }
+        }
+      }
+      advance();
     }
   }
   tc::fence_before_sync();
