@@ -1238,6 +1238,36 @@ pa_status check_rowbuf3(const pa_tensor* t, int32_t dtype, int64_t n0, int64_t n
   return t->shape[2] > INT32_MAX ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
+// Chooses the tokens of rows of at most n_max: the cluster size doubles (up
+// to 8) while the grid has fewer CTAs than two per SM and a CTA more than
+// 2048 tokens, or while a CTA's tokens do not fit its shared memory.
+pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceInfo& di, int dev, cudaStream_t s) {
+  const int64_t rows = int64_t(a.B) * a.Hkv;
+  const int64_t room = (int64_t(di.smem_optin) - int64_t(sizeof(pa::SelectSmem))) / 4;
+  int C = 1;
+  auto chunk = [&]() { return ((n_max + C - 1) / C + 31) / 32 * 32; };
+  while (C < 8 && (chunk() > room || (rows * C < 2 * int64_t(di.sms) && chunk() > 2048))) C *= 2;
+  const bool in_smem = chunk() <= room;
+  const size_t smem = sizeof(pa::SelectSmem) + (in_smem ? size_t(chunk()) * 4 : 0);
+  auto kern = in_smem ? pa::evict_select_kernel<true> : pa::evict_select_kernel<false>;
+  static std::atomic<size_t> smem_limit[2][kMaxDevices];
+  if (!raise_smem_limit(kern, smem, dev, smem_limit[in_smem])) return PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(C), unsigned(a.Hkv), unsigned(a.B));
+  cfg.blockDim = dim3(chunk() <= 4096 ? 256 : 512);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(C);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, int(chunk())) == cudaSuccess ? PA_OK : launch_status();
+}
+
 template <int G>
 cudaError_t run_accumulate(const pa::AccumArgs& a, dim3 grid, cudaStream_t s) {
   return launch_pdl(pa::accumulate_scores_kernel<G>, grid, dim3(256), 0, s, true, a);
@@ -1379,14 +1409,25 @@ pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   a.sink = num_sink, a.recent = num_recent;
   a.vpr = int32_t(k_cache->shape[3] * esize(k_cache->dtype) / 16);
   cudaStream_t s = stream_of(opts);
-  if (launch_pdl(pa::evict_select_kernel, dim3(unsigned(Hkv), unsigned(B)), dim3(pa::kSelThreads), 0, s, true, a) !=
-      cudaSuccess)
-    return launch_status();
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
+  if ((st = run_evict_select(a, std::min<int64_t>(max_nb * pa::kBS, a.S), di, dev, s)) != PA_OK) return st;
+  cudaError_t err;
   const int64_t rows = B * Hkv;
-  int64_t gx = (int64_t(di.sms) * 16 + rows - 1) / rows;
-  gx = std::min<int64_t>(gx, (int64_t(a.P) * a.vpr + 255) / 256);
-  const cudaError_t err = launch_pdl(pa::evict_move_kernel, dim3(unsigned(std::max<int64_t>(gx, 1)), unsigned(Hkv),
-                                     unsigned(B)), dim3(256), 0, s, true, a);
+  // a warp moves 32 tokens at a time; at least 8 CTAs of 8 warps per SM
+  int64_t gx = std::min<int64_t>((int64_t(di.sms) * 8 + rows - 1) / rows, (int64_t(a.P) + 255) / 256);
+  const dim3 grid(unsigned(std::max<int64_t>(gx, 1)), unsigned(Hkv), unsigned(B));
+  switch (a.vpr) {
+    case 8:
+      err = launch_pdl(pa::evict_move_kernel<8>, grid, dim3(256), 0, s, true, a);
+      break;
+    case 16:
+      err = launch_pdl(pa::evict_move_kernel<16>, grid, dim3(256), 0, s, true, a);
+      break;
+    default:
+      err = launch_pdl(pa::evict_move_kernel<32>, grid, dim3(256), 0, s, true, a);
+      break;
+  }
   return err == cudaSuccess ? PA_OK : launch_status();
 }
 

@@ -277,6 +277,28 @@ def test_evict_long_rows(n, keep):
     evict_case(31, [n, 300], [keep, 200], 2, 64, "bf16", 4, 32)
 
 
+@pytest.mark.parametrize("n,keep", [(450_000, 3000), (900, 300)])
+def test_evict_rows_longer_than_shared_memory(n, keep):
+    """A table and score rows of over 440,000 tokens: the scores are read from memory in every pass."""
+    ctx, hk, D = [n, 50], 1, 64
+    c = Case(33, ctx, hk, hk, D, "bf16", spare=-(-keep // 16) + 4, S=480_000)
+    table = np.full((2, 30_000), -1, np.int32)
+    table[:, :c.max_nb] = c.tables[:, :30_000]
+    dst = np.full((2, -(-keep // 16)), -1, np.int32)
+    dst[0] = c.free[:dst.shape[1]]
+    dst[1, 0] = c.free[dst.shape[1]]
+    d = c.device()
+    so, ko = torch.zeros(2, hk, keep, device=DEV), torch.zeros(2, hk, keep, dtype=torch.int32, device=DEV)
+    pa.pa_evict(d["kc"], d["vc"], torch.from_numpy(table).to(DEV), d["cl"], d["scores"],
+                torch.from_numpy(dst).to(DEV), torch.tensor([keep, 16], dtype=torch.int32, device=DEV), 1, 5, so, ko)
+    torch.cuda.synchronize()
+    check_status_clean()
+    k2, v2, s2, p2 = evict(as_bytes(c.kc), as_bytes(c.vc), c.tables, c.ctx, c.scores.numpy(), dst, [keep, 16], 1, 5,
+                           so.cpu().numpy(), ko.cpu().numpy())
+    assert np.array_equal(ko.cpu().numpy(), p2) and np.array_equal(so.cpu().numpy(), s2)
+    assert np.array_equal(as_bytes(d["kc"]), k2) and np.array_equal(as_bytes(d["vc"]), v2)
+
+
 def test_evict_keeps_scores_that_differ_in_one_bit():
     """Neighbouring floats: the choice goes by the last bit."""
     def make(c):
