@@ -1238,24 +1238,26 @@ pa_status check_rowbuf3(const pa_tensor* t, int32_t dtype, int64_t n0, int64_t n
   return t->shape[2] > INT32_MAX ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
-// Chooses the tokens of rows of at most n_max: the cluster size doubles (up
-// to 8) while the grid has fewer CTAs than two per SM and a CTA more than
-// 2048 tokens, or while a CTA's tokens do not fit its shared memory.
-pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceInfo& di, int dev, cudaStream_t s) {
+// Chooses the tokens of rows of at most n_max.  Up to 2048: one CTA of 256
+// threads a row, 8 keys each.  Up to 131072: a cluster of CTAs of 512
+// threads, 32 keys each, or 8 each while the grid has fewer CTAs than two per
+// SM.  Longer: a cluster of 8 that reads the scores again in every pass.
+pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceInfo& di, cudaStream_t s) {
   const int64_t rows = int64_t(a.B) * a.Hkv;
-  const int64_t room = (int64_t(di.smem_optin) - int64_t(sizeof(pa::SelectSmem))) / 4;
-  int C = 1;
-  auto chunk = [&]() { return ((n_max + C - 1) / C + 31) / 32 * 32; };
-  while (C < 8 && (chunk() > room || (rows * C < 2 * int64_t(di.sms) && chunk() > 2048))) C *= 2;
-  const bool in_smem = chunk() <= room;
-  const size_t smem = sizeof(pa::SelectSmem) + (in_smem ? size_t(chunk()) * 4 : 0);
-  auto kern = in_smem ? pa::evict_select_kernel<true> : pa::evict_select_kernel<false>;
-  static std::atomic<size_t> smem_limit[2][kMaxDevices];
-  if (!raise_smem_limit(kern, smem, dev, smem_limit[in_smem])) return PA_ERR_CUDA;
+  int C = 1, kpt = 8, threads = 256;
+  if (n_max > 2048) {
+    threads = 512;
+    kpt = 32;
+    while (C < 8 && int64_t(C) * threads * kpt < n_max) C *= 2;
+    int c8 = 1;
+    while (c8 < 8 && int64_t(c8) * threads * 8 < n_max) c8 *= 2;
+    if (int64_t(c8) * threads * 8 >= n_max && rows * C < 2 * int64_t(di.sms)) C = c8, kpt = 8;
+  }
+  const bool regs = int64_t(C) * threads * kpt >= n_max;
+  if (!regs) C = 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(C), unsigned(a.Hkv), unsigned(a.B));
-  cfg.blockDim = dim3(chunk() <= 4096 ? 256 : 512);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1265,7 +1267,16 @@ pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceIn
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, int(chunk())) == cudaSuccess ? PA_OK : launch_status();
+  cudaError_t err;
+  if (!regs)
+    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<0, 512, 2>, a, int((n_max + C - 1) / C));
+  else if (kpt == 32)
+    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<32, 512, 2>, a, 0);
+  else if (threads == 512)
+    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<8, 512, 2>, a, 0);
+  else
+    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<8, 256, 6>, a, 0);
+  return err == cudaSuccess ? PA_OK : launch_status();
 }
 
 template <int G>
@@ -1409,13 +1420,12 @@ pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   a.sink = num_sink, a.recent = num_recent;
   a.vpr = int32_t(k_cache->shape[3] * esize(k_cache->dtype) / 16);
   cudaStream_t s = stream_of(opts);
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
-  if ((st = run_evict_select(a, std::min<int64_t>(max_nb * pa::kBS, a.S), di, dev, s)) != PA_OK) return st;
+  if ((st = run_evict_select(a, std::min<int64_t>(max_nb * pa::kBS, a.S), di, s)) != PA_OK) return st;
   cudaError_t err;
   const int64_t rows = B * Hkv;
-  // a warp moves 32 tokens at a time; at least 8 CTAs of 8 warps per SM
-  int64_t gx = std::min<int64_t>((int64_t(di.sms) * 8 + rows - 1) / rows, (int64_t(a.P) + 255) / 256);
+  // a warp moves 32 tokens at a time: a CTA per 256 of the longest row, so
+  // that short rows do not leave long ones alone, within 64 CTAs per SM
+  int64_t gx = std::min<int64_t>((int64_t(di.sms) * 64 + rows - 1) / rows, (int64_t(a.P) + 255) / 256);
   const dim3 grid(unsigned(std::max<int64_t>(gx, 1)), unsigned(Hkv), unsigned(B));
   switch (a.vpr) {
     case 8:

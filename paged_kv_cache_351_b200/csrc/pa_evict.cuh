@@ -107,41 +107,48 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One cluster of C CTAs chooses for one (sequence, kv head): CTA r holds the
-// scores of tokens [r chunk, (r + 1) chunk) in shared memory (IN_SMEM; rows too
-// long for that are read again in every pass), so that a row is read once.
+// A cluster of C CTAs chooses for one (sequence, kv head), each warp over a run
+// of its tokens: their keys stay in registers, KPT a lane (rows of up to
+// 131072 tokens), or are read again in every pass (KPT = 0; a row stays in L2).
 //  * The threshold, the need-th largest key of the competing tokens, comes
-//    from a radix selection, 8 bits at a time: every CTA counts its keys that
-//    match the digits found so far, adds up the cluster's counts through
-//    distributed shared memory, and finds the digit by a suffix scan.  Hot
-//    digits (scores share their exponents) go to 8 copies of the counts, by
-//    lane.
-//  * Then each warp takes a run of tokens, counts those above the threshold
-//    and those at it, and with the sums before it (warps, then CTAs) writes
-//    its tokens that stay: position = above before + min(need, ties before).
-// Integer sums only: the choice is exact and does not depend on timing.
-// Bound by latency: a row is 4 bytes a token against 4 K/V rows of 128 to
-// 512 bytes for each that stays; the rule for C is in pa_evict.
+//    from a radix selection, 8 bits at a time below the keys' common prefix
+//    (scores share their sign and most of their exponent): every CTA counts
+//    its keys that match the digits found so far, the cluster's counts are
+//    added up through distributed shared memory, and a suffix scan finds the
+//    digit.  It ends early when a digit's keys stay all together, after two or
+//    three passes for scores that differ.  Hot digits go to 8 neighbouring
+//    copies of the count, by lane, so that a warp's lanes reach different
+//    banks.
+//  * Then every warp counts its tokens above the threshold and at it, and with
+//    the sums before it (warps, then CTAs) writes those that stay: position =
+//    above before + min(ties to keep, ties before).
+// Integer sums only: the choice is exact and does not depend on timing.  Bound
+// by the latency of these steps; a row is 4 bytes a token against four K/V
+// rows of 128 to 512 bytes for each token that stays.  (A search bit by bit
+// instead, a count and an exchange a bit, measured 42 us for the LLaMA
+// batch's 2048 rows and 146 us for 64 rows of 32 to 128 thousand tokens.)
 constexpr int kSelCopies = 8;
+static_assert(kSelCopies == 8, "read as two 16-byte vectors");
 
 struct SelectSmem {
-  unsigned int hist[kSelCopies][256];
+  uint4 hist[256][kSelCopies / 4];
   unsigned int tot[4][256];  // this CTA's counts of each pass
-  unsigned int warp_sum[32];
-  int gt[32], tie[32];       // per warp: tokens above the threshold, and at it
+  unsigned int warp_sum[8];
+  unsigned int all[16], any[16];  // per warp: and, or of its keys
+  int gt[16], tie[16];            // per warp: tokens above the threshold, and at it
+  unsigned int cta_all, cta_any;
   int cta_gt, cta_tie;
-  unsigned int digit, need;
+  unsigned int digit, need, exact;
 };
 
-template <bool IN_SMEM>
-__global__ void __launch_bounds__(512) evict_select_kernel(const EvictArgs a, int chunk) {
+template <int KPT, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const EvictArgs a, int chunk) {
   namespace cg = cooperative_groups;
-  extern __shared__ __align__(128) unsigned char smem[];
-  SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem);
-  float* const row = reinterpret_cast<float*>(smem + sizeof(SelectSmem));
+  __shared__ SelectSmem sm;
   cg::cluster_group cl = cg::this_cluster();
+  constexpr int NW = THREADS / 32;
   const int C = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
-  const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
   const int g = blockIdx.y, i = blockIdx.z;
@@ -153,43 +160,67 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictArgs a, in
   const float* sc = a.scores + i * a.s_sb + g * a.s_sh;
   float* so = a.scores_out + i * a.o_sb + g * a.o_sh;
   int32_t* kept = a.kept + i * a.k_sb + g * a.k_sh;
-  for (int t = s.K + rank * nthr + tid; t < a.So; t += C * nthr) so[t] = 0.f;
-  for (int t = s.K + rank * nthr + tid; t < a.P; t += C * nthr) kept[t] = -1;
-  if (s.K == s.n) {
-    for (int t = rank * nthr + tid; t < s.n; t += C * nthr) {
-      kept[t] = t;
-      so[t] = __ldg(sc + t);
-    }
-    return;
-  }
   const int lo = s.S0, hi = s.n - s.R;  // the tokens that compete
-  const int t0 = min(s.n, rank * chunk), t1 = min(s.n, t0 + chunk);
-  if constexpr (IN_SMEM) {
-#pragma unroll 4
-    for (int t = t0 + tid; t < t1; t += nthr) row[t - t0] = __ldg(sc + t);
+  // this warp's run: [w0, w0 + run)
+  const int run = KPT > 0 ? 32 * KPT : (chunk + NW - 1) / NW;
+  const int w0 = KPT > 0 ? (rank * NW + warp) * run : min(s.n, rank * chunk + warp * run);
+  auto load = [&](int t) { return t >= lo && t < hi ? score_key(__ldg(sc + t)) : 0u; };  // 0: does not compete
+  uint32_t key[KPT > 0 ? KPT : 1];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) key[k] = load(w0 + 32 * k + lane);
   }
-  auto score = [&](int t) { return IN_SMEM ? row[t - t0] : __ldg(sc + t); };
+  auto each = [&](auto&& f) {  // f(token, key) for the run, the warp together
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) f(w0 + 32 * k + lane, key[k]);
+    } else {
+      const int end = min(min(w0 + run, (rank + 1) * chunk), s.n);
+      for (int t = w0; t < end; t += 32) f(t + lane, t + lane < end ? load(t + lane) : 0u);
+    }
+  };
+  for (int t = s.K + rank * THREADS + tid; t < a.So; t += C * THREADS) so[t] = 0.f;
+  for (int t = s.K + rank * THREADS + tid; t < a.P; t += C * THREADS) kept[t] = -1;
 
   unsigned int need = unsigned(s.K - s.R - s.S0);
-  uint32_t thr = 0;  // the smallest key that stays; need: how many tokens of exactly that key do
-  const bool none = need == 0;
-  if (!none) {
-    const int c0 = max(t0, lo), c1 = min(t1, hi);
-    for (int p = 0; p < 4; ++p) {
-      const int shift = 24 - 8 * p;
-      for (int b = tid; b < kSelCopies * 256; b += nthr) (&sm.hist[0][0])[b] = 0;
+  uint32_t thr = need == 0 ? 0xffffffffu : 0u;  // keys above thr stay, and the first `ties` of those equal to it
+  unsigned int ties = need == 0 ? 0u : 0xffffffffu;
+  if (need > 0 && s.K < s.n) {
+    // ---- the keys' common prefix ----
+    uint32_t all = 0xffffffffu, any = 0u;
+    each([&](int, uint32_t k) {
+      if (k != 0u) all &= k;
+      any |= k;
+    });
+    all = __reduce_and_sync(0xffffffffu, all);
+    any = __reduce_or_sync(0xffffffffu, any);
+    if (lane == 0) sm.all[warp] = all, sm.any[warp] = any;
+    __syncthreads();
+    all = __reduce_and_sync(0xffffffffu, lane < NW ? sm.all[lane] : 0xffffffffu);
+    any = __reduce_or_sync(0xffffffffu, lane < NW ? sm.any[lane] : 0u);
+    if (C > 1) {
+      if (tid == 0) sm.cta_all = all, sm.cta_any = any;
+      cl.sync();
+      all = __reduce_and_sync(0xffffffffu, lane < C ? *cl.map_shared_rank(&sm.cta_all, lane) : 0xffffffffu);
+      any = __reduce_or_sync(0xffffffffu, lane < C ? *cl.map_shared_rank(&sm.cta_any, lane) : 0u);
+    }
+    int left = 32 - __clz(all ^ any);  // bits below the prefix
+    thr = left == 32 ? 0u : all & ~((1u << left) - 1u);
+    // ---- digit by digit ----
+    for (int p = 0; left > 0; ++p) {
+      const int bits = min(8, left), shift = left - bits;
+      for (int b = tid; b < 256 * kSelCopies / 4; b += THREADS) (&sm.hist[0][0])[b] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
-      for (int t = c0 + tid; t < c1; t += nthr) {
-        const uint32_t k = score_key(score(t));
-        if (p == 0 || (k >> (shift + 8)) == (thr >> (shift + 8)))
-          atomicAdd(&sm.hist[lane & (kSelCopies - 1)][(k >> shift) & 255u], 1u);
-      }
+      unsigned int* const mine = reinterpret_cast<unsigned int*>(&sm.hist[0][0]) + (lane & (kSelCopies - 1));
+      const uint32_t prefix = left == 32 ? 0u : thr >> left;
+      each([&](int, uint32_t k) {
+        if (k != 0u && (p == 0 || (k >> left) == prefix))
+          atomicAdd(mine + ((k >> shift) & ((1u << bits) - 1u)) * kSelCopies, 1u);
+      });
       __syncthreads();
       if (tid < 256) {
-        unsigned int n = 0;
-#pragma unroll
-        for (int c = 0; c < kSelCopies; ++c) n += sm.hist[c][tid];
-        sm.tot[p][tid] = n;
+        const uint4 x = sm.hist[tid][0], y = sm.hist[tid][1];
+        sm.tot[p][tid] = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
       }
       if (C > 1)
         cl.sync();
@@ -202,6 +233,7 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictArgs a, in
         if (C == 1) {
           n = sm.tot[p][d];
         } else {
+#pragma unroll 8
           for (int r = 0; r < C; ++r) n += cl.map_shared_rank(&sm.tot[p][0], r)[d];
         }
         suf = n;
@@ -218,70 +250,69 @@ __global__ void __launch_bounds__(512) evict_select_kernel(const EvictArgs a, in
         if (suf >= need && suf - n < need) {
           sm.digit = 255 - tid;
           sm.need = need - (suf - n);
+          sm.exact = suf == need;
         }
       }
       __syncthreads();
       thr |= sm.digit << shift;
       need = sm.need;
+      left = shift;
+      if (sm.exact) break;  // every key from thr on stays
+      if (left == 0) ties = need;
     }
-  } else {
-    __syncthreads();
+    if (all == any) ties = need;  // one key only
   }
 
-  // each warp's run of tokens, 32 at a time
-  const int per = ((t1 - t0 + nw - 1) / nw + 31) / 32 * 32;
-  const int w0 = min(t1, t0 + warp * per), w1 = min(t1, w0 + per);
-  auto classify = [&](int t, float x, bool& gt, bool& tie) {
-    const bool in = t < w1, mid = t >= lo && t < hi;
-    const uint32_t k = score_key(x);
-    gt = in && (!mid || (!none && k > thr));
-    tie = in && mid && !none && k == thr;
+  // ---- positions ----
+  const uint32_t below = (1u << lane) - 1u;
+  auto classify = [&](int t, uint32_t k, bool& gt, bool& tie) {
+    const bool mid = t >= lo && t < hi;
+    gt = t < s.n && (!mid || k > thr);
+    tie = mid && k == thr;
   };
   int n_gt = 0, n_tie = 0;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
+  each([&](int t, uint32_t k) {
     bool gt, tie;
-    classify(t, t < w1 ? score(t) : 0.f, gt, tie);
+    classify(t, k, gt, tie);
     n_gt += __popc(__ballot_sync(0xffffffffu, gt));
     n_tie += __popc(__ballot_sync(0xffffffffu, tie));
-  }
+  });
   if (lane == 0) {
     sm.gt[warp] = n_gt;
     sm.tie[warp] = n_tie;
   }
   __syncthreads();
-  int b_gt = 0, b_tie = 0;
+  int b_gt = 0;
+  unsigned int b_tie = 0;
   for (int w = 0; w < warp; ++w) {
     b_gt += sm.gt[w];
     b_tie += sm.tie[w];
   }
   if (C > 1) {
-    if (tid == nthr - 1) {
+    if (tid == THREADS - 1) {
       sm.cta_gt = b_gt + n_gt;
-      sm.cta_tie = b_tie + n_tie;
+      sm.cta_tie = int(b_tie) + n_tie;
     }
     cl.sync();
     for (int r = 0; r < rank; ++r) {
       b_gt += *cl.map_shared_rank(&sm.cta_gt, r);
       b_tie += *cl.map_shared_rank(&sm.cta_tie, r);
     }
-    // no CTA leaves while another reads its counts
-    cl.sync();
+    cl.sync();  // no CTA leaves while another reads its counts
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
+  each([&](int t, uint32_t k) {
     bool gt, tie;
-    const float x = t < w1 ? score(t) : 0.f;
-    classify(t, x, gt, tie);
+    classify(t, k, gt, tie);
     const uint32_t m_gt = __ballot_sync(0xffffffffu, gt), m_tie = __ballot_sync(0xffffffffu, tie);
-    const int before = b_tie + __popc(m_tie & below);
-    if (gt || (tie && before < int(need))) {
-      const int pos = b_gt + __popc(m_gt & below) + min(int(need), before);
+    const unsigned int before = b_tie + __popc(m_tie & below);
+    if (gt || (tie && before < ties)) {
+      const int pos = b_gt + __popc(m_gt & below) + int(min(ties, before));
       kept[pos] = t;
-      so[pos] = x;
+      so[pos] = __ldg(sc + t);
     }
     b_gt += __popc(m_gt);
     b_tie += __popc(m_tie);
-  }
+  });
 }
 
 // ---- move -----------------------------------------------------------------------

@@ -255,7 +255,8 @@ def test_evict(dtype, D, hk, sink, recent):
 
 
 @pytest.mark.parametrize("kind", ["zeros", "few values", "special", "one value above"])
-def test_evict_ties_and_special_scores(kind):
+@pytest.mark.parametrize("longest", [700, 1500, 5000])  # a warp a row (32, 64 keys a lane), a cluster a row
+def test_evict_ties_and_special_scores(kind, longest):
     def make(c):
         g = torch.Generator().manual_seed(1)
         s = torch.zeros_like(c.scores)
@@ -269,10 +270,11 @@ def test_evict_ties_and_special_scores(kind):
         return s
 
     for sink, recent in ((0, 0), (4, 10)):
-        evict_case(21, [700, 64, 33, 100], [350, 20, 32, 7], 2, 64, "bf16", sink, recent, scores=make)
+        evict_case(21, [longest, 64, 33, 100], [longest // 2, 20, 32, 7], 2, 64, "bf16", sink, recent, scores=make)
 
 
-@pytest.mark.parametrize("n,keep", [(20000, 2500), (5000, 4999), (70000, 37)])
+@pytest.mark.parametrize("n,keep", [(1024, 1000), (1025, 3), (2048, 1024), (2049, 2048), (20000, 2500), (5000, 4999),
+                                    (70000, 37), (40000, 0), (40000, 36)])
 def test_evict_long_rows(n, keep):
     evict_case(31, [n, 300], [keep, 200], 2, 64, "bf16", 4, 32)
 
