@@ -104,7 +104,7 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictArgs& a, int i) {
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) x = -INFINITY;
   const uint32_t u = __float_as_uint(x + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
 
 // A cluster of C CTAs chooses for one (sequence, kv head), each warp over a run
@@ -123,7 +123,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 //    the sums before it (warps, then CTAs) writes those that stay: position =
 //    above before + min(ties to keep, ties before).
 // Integer sums only: the choice is exact and does not depend on timing.  Bound
-// by the latency of these steps; a row is 4 bytes a token against four K/V
+// by the instructions and the latency of these steps; a row is 4 bytes a token against four K/V
 // rows of 128 to 512 bytes for each token that stays.  (A search bit by bit
 // instead, a count and an exchange a bit, measured 42 us for the LLaMA
 // batch's 2048 rows and 146 us for 64 rows of 32 to 128 thousand tokens.)
@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
   // this warp's run: [w0, w0 + run)
   const int run = KPT > 0 ? 32 * KPT : (chunk + NW - 1) / NW;
   const int w0 = KPT > 0 ? (rank * NW + warp) * run : min(s.n, rank * chunk + warp * run);
-  auto load = [&](int t) { return t >= lo && t < hi ? score_key(__ldg(sc + t)) : 0u; };  // 0: does not compete
+  const unsigned int mids = unsigned(hi - lo);
+  auto load = [&](int t) { return unsigned(t - lo) < mids ? score_key(__ldg(sc + t)) : 0u; };  // 0: does not compete
   uint32_t key[KPT > 0 ? KPT : 1];
   if constexpr (KPT > 0) {
 #pragma unroll
@@ -264,19 +265,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
   }
 
   // ---- positions ----
+  // Bit k of a lane's masks: its k-th token is above the threshold (or
+  // protected), or at it.  (KPT = 0: 32 tokens a lane at a time.)
   const uint32_t below = (1u << lane) - 1u;
-  auto classify = [&](int t, uint32_t k, bool& gt, bool& tie) {
-    const bool mid = t >= lo && t < hi;
-    gt = t < s.n && (!mid || k > thr);
-    tie = mid && k == thr;
-  };
+  auto is_tie = [&](int t, uint32_t k) { return k == thr && unsigned(t - lo) < mids; };
+  auto is_gt = [&](int t, uint32_t k) { return k > thr || (t < s.n && unsigned(t - lo) >= mids); };
   int n_gt = 0, n_tie = 0;
   each([&](int t, uint32_t k) {
-    bool gt, tie;
-    classify(t, k, gt, tie);
-    n_gt += __popc(__ballot_sync(0xffffffffu, gt));
-    n_tie += __popc(__ballot_sync(0xffffffffu, tie));
+    n_gt += is_gt(t, k);
+    n_tie += is_tie(t, k);
   });
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_tie = __reduce_add_sync(0xffffffffu, n_tie);
   if (lane == 0) {
     sm.gt[warp] = n_gt;
     sm.tie[warp] = n_tie;
@@ -300,18 +300,27 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
     }
     cl.sync();  // no CTA leaves while another reads its counts
   }
+  int done = b_gt + int(min(ties, b_tie));  // tokens that stay before this warp's
+  // the ties of this warp all stay, or none does, or it holds the last that do
+  const bool all_ties = b_tie + n_tie <= ties, no_ties = n_tie == 0 || b_tie >= ties;
   each([&](int t, uint32_t k) {
-    bool gt, tie;
-    classify(t, k, gt, tie);
-    const uint32_t m_gt = __ballot_sync(0xffffffffu, gt), m_tie = __ballot_sync(0xffffffffu, tie);
-    const unsigned int before = b_tie + __popc(m_tie & below);
-    if (gt || (tie && before < ties)) {
-      const int pos = b_gt + __popc(m_gt & below) + int(min(ties, before));
+    bool stay = is_gt(t, k);
+    if (!no_ties) {
+      bool tie = is_tie(t, k);
+      if (!all_ties) {
+        const uint32_t m = __ballot_sync(0xffffffffu, tie);
+        tie = tie && b_tie + __popc(m & below) < ties;
+        b_tie += __popc(m);
+      }
+      stay |= tie;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, stay);
+    if (stay) {
+      const int pos = done + __popc(m & below);
       kept[pos] = t;
       so[pos] = __ldg(sc + t);
     }
-    b_gt += __popc(m_gt);
-    b_tie += __popc(m_tie);
+    done += __popc(m);
   });
 }
 
@@ -319,7 +328,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
 // K/V of kept token j of (sequence, kv head) -> position j of the destination
 // table.  Pure copy.  A warp takes 32 kept tokens: lane l looks up token l's
 // source and destination rows once, then the rows go 32 / VPR at a time as
-// 16-byte vectors, four steps' K and V loads in flight.
+// 16-byte vectors, four steps' K and V loads in flight.  (One kernel for the
+// choice and the move, a CTA a row, measured slower on the LLaMA batch, 0.193
+// against 0.164 + 0.025 ms: the longest rows are 40 times the shortest.)
 template <int VPR>  // 16-byte vectors per row
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   pdl_wait();

@@ -442,8 +442,9 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 // ever overwritten after it was read, in the order k = 0, 1, ...  One thread
 // owns one 16-byte column of a (sequence, head) and walks its path: no two
 // threads touch the same bytes, so the walk needs no synchronisation.  Pure
-// copy; bound by the latency of two dependent rounds (the path and the block
-// ids, then the rows), so kCommitBatch rows are loaded at once.
+// copy of a few rows a sequence, bound by the latency of its dependent steps
+// (lengths, path, block ids, rows): lane k of each warp looks step k of the
+// path up, 32 at a time, and kCommitBatch rows are loaded at once.
 constexpr int kCommitBatch = 8;
 
 struct CommitArgs {
@@ -462,50 +463,66 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const CommitArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int per_seq = a.Hkv * 2 * a.vpr;
-  const int i = blockIdx.y;
+  const int i = blockIdx.y, lane = threadIdx.x & 31;
   const int id = blockIdx.x * blockDim.x + threadIdx.x;
-  if (id >= per_seq) return;
-  const int c = id % a.vpr, kv = (id / a.vpr) & 1, h = id / (2 * a.vpr);
   const int count = __ldg(a.count + i);
-  if (count == 0) return;
   const int64_t n = int64_t(__ldg(a.qs + i + 1)) - __ldg(a.qs + i);
   const int ctx = __ldg(a.ctx + i);
+  if (count == 0) return;
   const int32_t* acc = a.acc + int64_t(i) * a.acc_stride;
+  const int32_t* bt = a.bt + int64_t(i) * a.bt_stride;
   bool ok = count > 0 && count <= a.P && n >= count && n <= ctx && ctx <= a.max_nb * kBS;
-  int last = -1;
-  for (int k = 0; ok && k < count; ++k) {
-    const int u = __ldg(acc + k);
-    ok = u > last && u < n;
-    last = u;
-  }
-  if (!ok) {
-    if (id == 0) flag(PA_DEV_BAD_CONTEXT);
+  const int c0 = ctx - int(n);
+  // The whole path first: strictly ascending in [0, n), every block in the
+  // pool; else nothing of the sequence moves.  (Steps the next round reads
+  // again; a path rarely has over 32.)
+  int u = 0;
+  bool blocks_ok = true;
+  int64_t src = 0, dst = 0;  // this lane's step: row indices of head 0
+  auto step = [&](int k0) {
+    const int k = k0 + lane;
+    bool good = true;
+    u = k;
+    if (k < count) {
+      u = __ldg(acc + k);
+      good = u >= k && u < n && (k == 0 || __ldg(acc + k - 1) < u);
+      if (good) {
+        const int sb = __ldg(bt + (c0 + u) / kBS), db = __ldg(bt + (c0 + k) / kBS);
+        blocks_ok &= unsigned(sb) < unsigned(a.num_blocks) && unsigned(db) < unsigned(a.num_blocks);
+        src = int64_t(sb) * a.Hkv * kBS + (c0 + u) % kBS;
+        dst = int64_t(db) * a.Hkv * kBS + (c0 + k) % kBS;
+      }
+    }
+    return __all_sync(0xffffffffu, good);
+  };
+  // the last round first, so that a path of one round is looked up once
+  const int last = ok ? (count - 1) / 32 * 32 : 0;
+  for (int k0 = last; ok && k0 >= 0; k0 -= 32) ok = step(k0);
+  blocks_ok = __all_sync(0xffffffffu, blocks_ok);
+  if (!ok || !blocks_ok) {
+    if (id == 0) flag(ok ? PA_DEV_BAD_BLOCK : PA_DEV_BAD_CONTEXT);
     return;
   }
-  const int c0 = ctx - int(n);
-  const int32_t* bt = a.bt + int64_t(i) * a.bt_stride;
-  // every block of the path is in the pool, or nothing of the sequence moves
-  for (int b = c0 / kBS; b <= (c0 + last) / kBS; ++b) {
-    if (unsigned(__ldg(bt + b)) >= unsigned(a.num_blocks)) {
-      if (id == 0) flag(PA_DEV_BAD_BLOCK);
-      return;
-    }
-  }
-  uint4* cache = kv ? a.vc : a.kc;
-  auto at = [&](int pos) {
-    return cache + ((int64_t(__ldg(bt + pos / kBS)) * a.Hkv + h) * kBS + pos % kBS) * a.vpr + c;
-  };
-  for (int k0 = 0; k0 < count; k0 += kCommitBatch) {
-    uint4 row[kCommitBatch];
-    int u[kCommitBatch];
+  const int c = id % a.vpr, kv = (id / a.vpr) & 1, h = id / (2 * a.vpr);
+  uint4* const col = (kv ? a.vc : a.kc) + int64_t(h) * kBS * a.vpr + c;
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    if (k0 > 0) step(k0);
+    for (int k1 = 0; k1 < 32 && k0 + k1 < count; k1 += kCommitBatch) {
+      uint4 row[kCommitBatch];
+      int64_t to[kCommitBatch];
+      bool move[kCommitBatch];
 #pragma unroll
-    for (int k = 0; k < kCommitBatch; ++k) {
-      u[k] = k0 + k < count ? __ldg(acc + k0 + k) : k0 + k;
-      if (u[k] != k0 + k) row[k] = __ldcg(at(c0 + u[k]));
-    }
+      for (int k = 0; k < kCommitBatch; ++k) {
+        const int64_t from = __shfl_sync(0xffffffffu, src, k1 + k) * a.vpr;
+        to[k] = __shfl_sync(0xffffffffu, dst, k1 + k) * a.vpr;
+        const int at = __shfl_sync(0xffffffffu, u, k1 + k);  // (every lane, also those past the last column)
+        move[k] = id < per_seq && at != k0 + k1 + k;
+        if (move[k]) row[k] = __ldcg(col + from);
+      }
 #pragma unroll
-    for (int k = 0; k < kCommitBatch; ++k)
-      if (u[k] != k0 + k) *at(c0 + k0 + k) = row[k];
+      for (int k = 0; k < kCommitBatch; ++k)
+        if (move[k]) col[to[k]] = row[k];
+    }
   }
 }
 

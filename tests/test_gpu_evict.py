@@ -279,6 +279,16 @@ def test_evict_long_rows(n, keep):
     evict_case(31, [n, 300], [keep, 200], 2, 64, "bf16", 4, 32)
 
 
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_evict_many_rows(dtype, D):
+    """Over four rows per SM: the kernel that chooses also moves."""
+    rng = np.random.default_rng(35)
+    ctx = [int(x) for x in rng.integers(0, 60, 150)]
+    keep = [int(x) for x in rng.integers(0, 60, 150)]
+    ctx[7], keep[7] = 1500, 700
+    evict_case(35, ctx, keep, 5, D, dtype, 2, 5, pad=(3, 2))
+
+
 @pytest.mark.parametrize("n,keep", [(450_000, 3000), (900, 300)])
 def test_evict_rows_longer_than_shared_memory(n, keep):
     """A table and score rows of over 440,000 tokens: the scores are read from memory in every pass."""

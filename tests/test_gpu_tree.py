@@ -343,6 +343,33 @@ def test_commit_moves_the_path(dtype, D, hk):
         assert np.array_equal(as_bytes(got), want)
 
 
+@pytest.mark.parametrize("hk", [1, 5])
+def test_commit_long_paths(hk):
+    """Paths over several rounds of 32, and ones that move nothing or one row far on."""
+    pairs = [(7, 200), (16, 100), (0, 65), (40, 64), (3, 97)]
+    rng = np.random.default_rng(5)
+    paths = [sorted(rng.choice(200, 131, replace=False).tolist()), list(range(33)) + [99], list(range(65)),
+             list(range(1, 64)), list(range(32)) + [40, 96]]
+    c = Case(47, pairs, hk, hk, 128, "bf16")
+    d = c.device()
+    acc = torch.zeros(len(pairs), 131, dtype=torch.int32)
+    for i, p in enumerate(paths):
+        acc[i, :len(p)] = torch.tensor(p, dtype=torch.int32)
+    cnt = torch.tensor([len(p) for p in paths], dtype=torch.int32, device=DEV)
+    pa.pa_tree_commit(d["kc"], d["vc"], d["bt"], d["cl"], d["qs"], acc.to(DEV), cnt)
+    check_status_clean()
+    for got, src in ((d["kc"], c.kc), (d["vc"], c.vc)):
+        assert np.array_equal(as_bytes(got), tree_commit(as_bytes(src), c.tables, c.ctx, c.n, paths))
+    # a fault in the second round: nothing moves
+    d = c.device()
+    acc[0, 40] = acc[0, 39]
+    pa.pa_tree_commit(d["kc"], d["vc"], d["bt"], d["cl"], d["qs"], acc.to(DEV), cnt)
+    st, bits = pa.pa_get_device_status()
+    assert bits == pa.PA_DEV_BAD_CONTEXT
+    want = tree_commit(as_bytes(c.kc), c.tables, c.ctx, c.n, [[]] + paths[1:])
+    assert np.array_equal(as_bytes(d["kc"]), want)
+
+
 def test_commit_refuses_bad_paths():
     """A path that does not ascend, leaves the draft or is too long, and a bad
     block: reported, and nothing of the sequence moves; the others do."""
