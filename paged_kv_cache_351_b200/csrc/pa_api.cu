@@ -1351,10 +1351,11 @@ pa_status pa_decode_scored(pa_tensor* out, pa_tensor* scores, const pa_tensor* q
   c.s_sb = dc.B > 1 ? scores->stride[0] : 0;
   c.s_sh = dc.Hkv > 1 ? scores->stride[1] : 0;
   c.B = int32_t(dc.B), c.Hkv = int32_t(dc.Hkv), c.cap = int32_t(cap), c.S = int32_t(scores->shape[2]);
-  // enough blocks for 8 per SM, each striding over its row's tokens
+  // a CTA per kAccTokens of the longest row, so that short rows do not leave
+  // long ones alone, within 64 CTAs per SM
   const int64_t rows = dc.B * dc.Hkv;
-  int64_t gx = (int64_t(di.sms) * 8 + rows - 1) / rows;
-  gx = std::min<int64_t>(gx, (cap + 255) / 256);
+  const int64_t gx = std::min<int64_t>((int64_t(di.sms) * 64 + rows - 1) / rows,
+                                       (cap + pa::kAccTokens - 1) / pa::kAccTokens);
   const dim3 grid(unsigned(std::max<int64_t>(gx, 1)), unsigned(dc.Hkv), unsigned(dc.B));
   cudaError_t err;
   switch (dc.G) {

@@ -28,6 +28,8 @@ struct AccumArgs {
   int32_t B, Hkv, cap, S;
 };
 
+constexpr int kAccTokens = 1024;  // per CTA and round
+
 template <int G>
 __global__ void __launch_bounds__(256) accumulate_scores_kernel(const AccumArgs a) {
   pdl_wait();
@@ -38,29 +40,42 @@ __global__ void __launch_bounds__(256) accumulate_scores_kernel(const AccumArgs 
     if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0) flag(PA_DEV_BAD_CONTEXT);
     n = a.S;
   }
+  if (int(blockIdx.x) * kAccTokens >= n) return;
   float lse[G];
 #pragma unroll
   for (int j = 0; j < G; ++j) lse[j] = a.lse[(int64_t(i) * a.Hkv + g) * G + j];
   const float* lg = a.logits + (int64_t(i) * a.Hkv + g) * a.cap * G;
   float* sc = a.scores + i * a.s_sb + g * a.s_sh;
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
-    float x[G];
-    if constexpr (G >= 4) {
+  // four tokens a thread, their loads in flight together
+  for (int t0 = blockIdx.x * kAccTokens + threadIdx.x; t0 < n; t0 += gridDim.x * kAccTokens) {
+    float x[4][G], old[4];
 #pragma unroll
-      for (int j = 0; j < G; j += 4) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(lg + int64_t(t) * G + j));
-        x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+    for (int k = 0; k < 4; ++k) {
+      const int t = t0 + k * 256;
+      if (t >= n) continue;
+      old[k] = sc[t];
+      const float* src = lg + int64_t(t) * G;
+      if constexpr (G >= 4) {
+#pragma unroll
+        for (int j = 0; j < G; j += 4) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(src + j));
+          x[k][j] = v.x, x[k][j + 1] = v.y, x[k][j + 2] = v.z, x[k][j + 3] = v.w;
+        }
+      } else if constexpr (G == 2) {
+        const float2 v = __ldcs(reinterpret_cast<const float2*>(src));
+        x[k][0] = v.x, x[k][1] = v.y;
+      } else {
+        x[k][0] = __ldcs(src);
       }
-    } else if constexpr (G == 2) {
-      const float2 v = __ldcs(reinterpret_cast<const float2*>(lg + int64_t(t) * G));
-      x[0] = v.x, x[1] = v.y;
-    } else {
-      x[0] = __ldcs(lg + t);
     }
-    float w = 0.f;
 #pragma unroll
-    for (int j = 0; j < G; ++j) w += ex2(x[j] - lse[j]);
-    sc[t] += w;
+    for (int k = 0; k < 4; ++k) {
+      if (t0 + k * 256 >= n) continue;
+      float w = 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j) w += ex2(x[k][j] - lse[j]);
+      sc[t0 + k * 256] = old[k] + w;
+    }
   }
 }
 
