@@ -1133,7 +1133,7 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   a.o_st = out->stride[0], a.o_sh = out->stride[1];
   a.bt_stride = B > 1 ? block_tables->stride[0] : 0;
   a.mask_stride = T > 1 ? tree_mask->stride[0] : 0;
-  a.B = int32_t(B), a.T = int32_t(T), a.Hkv = int32_t(Hkv), a.G = int32_t(G), a.max_nb = int32_t(max_nb);
+  a.B = int32_t(B), a.T = int32_t(T), a.Hkv = int32_t(Hkv), a.lg = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3, a.max_nb = int32_t(max_nb);
   a.num_blocks = int32_t(NB), a.words = int32_t(tree_mask->shape[1]), a.max_q = max_query_len;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.timeout_ns = timeout_of(opts);

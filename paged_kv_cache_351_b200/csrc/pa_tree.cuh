@@ -36,7 +36,7 @@ struct TreeArgs {
   const int32_t* qs;    // [B + 1] first row of each sequence
   const uint32_t* mask; // [T, words]
   int64_t q_st, q_sh, o_st, o_sh, bt_stride, mask_stride;
-  int32_t B, T, Hkv, G, max_nb, num_blocks, words, max_q;
+  int32_t B, T, Hkv, lg, max_nb, num_blocks, words, max_q;  // lg: log2 of the query heads per kv head
   float scale_log2;  // scale * log2(e)
   int32_t split;     // 1: units may be cut between workers (shares below)
   float* sh_o;       // shares: two slots per worker, [R][D] floats each
@@ -61,11 +61,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int i) {
   return TreeSeq{int(q0), int(n), ctx - int(n)};
 }
 
-// Position in the flattened list: sequence, unit of the sequence (kv head
-// major, row tile minor), position in the unit (LEAD, then its key tiles).
+// Position in the flattened list: sequence, kv head, row tile, position in
+// the unit (LEAD, then its key tiles).
 struct TreePos {
-  int i, u, p;
-  int units, nt;  // units of the sequence, key tiles of each
+  int i, h, rt, p;
+  int rts, nt;  // row tiles of each kv head of the sequence (0: no drafted rows), key tiles of each unit
   TreeSeq s;
 };
 
@@ -87,7 +87,7 @@ __device__ __forceinline__ TreeSeg tree_seg(const TreePos& x, int left) {
 template <int R, int KT>
 __device__ __forceinline__ void tree_shape(const TreeArgs& a, TreePos& x) {
   x.s = tree_seq(a, x.i);
-  x.units = a.Hkv * ((x.s.n * a.G + R - 1) / R);
+  x.rts = ((x.s.n << a.lg) + R - 1) / R;
   x.nt = x.s.n > 0 ? (x.s.c0 + x.s.n + KT - 1) / KT : 0;
 }
 
@@ -95,13 +95,15 @@ __device__ __forceinline__ void tree_shape(const TreeArgs& a, TreePos& x) {
 template <int R, int KT>
 __device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreePos& x) {
   x.p = 0;
-  if (++x.u < x.units) return;
-  x.u = 0;
+  if (++x.rt < x.rts) return;
+  x.rt = 0;
+  if (++x.h < a.Hkv) return;
+  x.h = 0;
   do {
     ++x.i;
     if (x.i >= a.B) return;
     tree_shape<R, KT>(a, x);
-  } while (x.units == 0);
+  } while (x.rts == 0);
 }
 
 // Whole block: this worker's range [lo, hi) of the list, the list's length, and the position of lo.  smem: 40 ints.
@@ -136,7 +138,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
     TreePos x;
     x.i = i;
     tree_shape<R, KT>(a, x);
-    local += x.units > 0 ? x.units * (x.nt + LEAD) : 0;
+    local += x.rts * a.Hkv * (x.nt + LEAD);
   }
   int total;
   const int first = block_exclusive_scan(local, smem, &total);
@@ -158,7 +160,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
         TreePos x;
         x.i = i;
         tree_shape<R, KT>(a, x);
-        const int len = x.nt + LEAD, t = x.units * len;
+        const int len = x.nt + LEAD, t = x.rts * a.Hkv * len;
         if (b < base + t) {
           const int off = b - base;
           smem[32 + 4 * e + 0] = i;
@@ -174,9 +176,10 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   __syncthreads();
   if (r.lo < r.W) {
     r.at.i = smem[32];
-    r.at.u = smem[33];
     r.at.p = smem[34];
     tree_shape<R, KT>(a, r.at);
+    r.at.h = smem[33] / r.at.rts;
+    r.at.rt = smem[33] - r.at.h * r.at.rts;
     r.lo -= smem[35];
   }
   if (r.hi < r.W) r.hi -= smem[39];
@@ -254,9 +257,8 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
       continue;
     }
-    const int rts = x.units / a.Hkv;
-    const int kvh = x.u / rts, r0 = (x.u % rts) * kTsRows;
-    const int rows = min(kTsRows, x.s.n * a.G - r0);
+    const int kvh = x.h, r0 = x.rt * kTsRows, gm = (1 << a.lg) - 1;
+    const int rows = min(kTsRows, (x.s.n << a.lg) - r0);
     const int kv_len = x.s.c0 + x.s.n;
     for (int e = threadIdx.x; e < kTsRows * VPR; e += blockDim.x) {
       const int r = e / VPR, c = e % VPR;
@@ -264,9 +266,9 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 #pragma unroll
       for (int k = 0; k < EPV; ++k) f[k] = 0.f;
       if (r < rows) {
-        const int tok = (r0 + r) / a.G, j = (r0 + r) % a.G;
+        const int tok = (r0 + r) >> a.lg, j = (r0 + r) & gm;
         Elem<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (x.s.q0 + tok) * a.q_st +
-                                                        (kvh * a.G + j) * a.q_sh + c * EPV),
+                                                        ((kvh << a.lg) + j) * a.q_sh + c * EPV),
                         f);
       }
 #pragma unroll
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int r = 0; r < RW; ++r) {
         const int row = r0 + warp * RW + r;
         seen[r] = 0xffffffffu;
-        if (tree) seen[r] = row < x.s.n * a.G ? tree_seen32(a, x.s.q0 + row / a.G, x.s.n, key0 - x.s.c0) : 0u;
+        if (tree) seen[r] = row < (x.s.n << a.lg) ? tree_seen32(a, x.s.q0 + (row >> a.lg), x.s.n, key0 - x.s.c0) : 0u;
         const bool vis = (seen[r] >> lane) & 1u;
         if (!vis) s[r] = -INFINITY;
         float mx = s[r];
@@ -420,12 +422,12 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int r = 0; r < RW; ++r) {
         if (warp * RW + r >= rows) continue;
         const int row = r0 + warp * RW + r;
-        const float inv = tree_inverse(a, l[r], x.s.c0, x.s.n, x.s.q0 + row / a.G);
+        const float inv = tree_inverse(a, l[r], x.s.c0, x.s.n, x.s.q0 + (row >> a.lg));
         float y[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) y[e] = o[r][e] * inv;
-        store_out_small<T, PER>(static_cast<T*>(a.out) + (x.s.q0 + row / a.G) * a.o_st +
-                                    (kvh * a.G + row % a.G) * a.o_sh + lane * PER,
+        store_out_small<T, PER>(static_cast<T*>(a.out) + (x.s.q0 + (row >> a.lg)) * a.o_st +
+                                    ((kvh << a.lg) + (row & gm)) * a.o_sh + lane * PER,
                                 y);
       }
     }

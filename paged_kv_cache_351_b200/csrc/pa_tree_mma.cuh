@@ -16,7 +16,8 @@
 //    drains, merges or waits for its softmax;
 //  * more rows: two halves that share every K/V tile in shared memory (the
 //    K/V bytes an SM pulls would otherwise double), KT = 128, one CTA per
-//    SM, the halves' products and softmaxes alternating.
+//    SM, the halves' products and softmaxes alternating; P V starts on the
+//    first half of a tile's keys while the softmax is at the second.
 // Roles: warp 0 loads K, warp 2 loads V, warp 3 loads Q (tiled TMA with
 // 128-byte swizzle; a page is a [16 tokens][64 dims] box per half of the head
 // dimension), warp 1 owns TMEM and issues the products, warps 4.. run the
@@ -80,7 +81,8 @@ enum TmBar : int {
   kTmDrain = 24,
   kTmBDone = 25,  // half B's warps have read a unit's results, 4 arrivals
   kTmSlot = 26,   // 4-byte TMEM base address
-  kTmLast = 27,   // + half * 4 bytes: this half completes a cut unit
+  kTmPPart = 27,  // + half (2), 128 arrivals: the first half of P's keys (two halves only)
+  kTmLast = 29,   // + half * 4 bytes: this half completes a cut unit
 };
 
 // bf16 pair: a mask of the halves (low 0xffff, high 0xffff0000) that are infinite or NaN.
@@ -91,10 +93,82 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
 // The four softmax warps of one half.
 __device__ __forceinline__ void half_sync(int hx) { asm volatile("bar.sync %0, 128;" ::"r"(1 + hx) : "memory"); }
 
+// The merge of a cut unit's shares, of ns workers from wa on, by the four warps
+// of a half (all their lanes): 32 rows x D / parts dims a warp, the weights
+// once, then 16 dims of up to four shares at a time.  Out of line, so that
+// its registers do not burden the softmax.
+template <int D, int HALVES>
+__device__ __noinline__ void tree_merge(const TreeArgs& a, const TreePos x, int wa, int ns, int hx, int quad,
+                                        int rows) {
+  const int lane = threadIdx.x & 31;
+  const int groups = (min(128, rows - hx * 128) + 31) / 32;
+  const int parts = groups == 1 ? 4 : groups == 2 ? 2 : 1;
+  const int r = quad % (4 / parts) * 32 + lane;
+  const int dl = D / parts * (quad / (4 / parts)), dh = dl + D / parts;
+  if (r / 32 >= groups) return;
+  auto slot_of = [&](int k) { return share_slot(wa + k, wa) * HALVES + hx; };
+  auto pair = [&](int k) {
+    return k < ns ? __ldcg(a.sh_ml + slot_of(k) * 128 + r) : make_float2(-INFINITY, 0.f);
+  };
+  float M = -INFINITY, L = 0.f;
+  for (int k0 = 0; k0 < ns; k0 += 4) {
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ml[k] = pair(k0 + k);
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    L *= ex2(M - mu);
+    M = mn;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) L += ml[k].y * ex2(ml[k].x - mu);
+  }
+  const float mu = M == -INFINITY ? 0.f : M;
+  const bool valid = hx * 128 + r < rows;
+  const int row = x.rt * TreeMma<D, HALVES>::R + hx * 128 + r, tk = valid ? row >> a.lg : 0;
+  const float inv = tree_inverse(a, L, x.s.c0, x.s.n, x.s.q0 + tk);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (x.s.q0 + tk) * a.o_st +
+                       ((x.h << a.lg) + (row & ((1 << a.lg) - 1))) * a.o_sh;
+#pragma unroll 1
+  for (int d0 = dl; d0 < dh; d0 += 16) {
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < ns; k0 += 4) {
+      float4 v[4][4];
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool on = k0 + k < ns;
+        w[k] = ex2(pair(k0 + k).x - mu);
+        const float4* src = reinterpret_cast<const float4*>(a.sh_o) + (slot_of(k0 + k) * (D / 4) + d0 / 4) * 128 + r;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[k][d] = on ? __ldcg(src + d * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          o[4 * d] = fmaf(w[k], v[k][d].x, o[4 * d]);
+          o[4 * d + 1] = fmaf(w[k], v[k][d].y, o[4 * d + 1]);
+          o[4 * d + 2] = fmaf(w[k], v[k][d].z, o[4 * d + 2]);
+          o[4 * d + 3] = fmaf(w[k], v[k][d].w, o[4 * d + 3]);
+        }
+    }
+    if (valid) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        reinterpret_cast<uint4*>(dst + d0)[e] = make_uint4(
+            pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+            pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+    }
+  }
+}
+
 template <int D, int HALVES>
 __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES>::CTAS)
     tree_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
   using C = TreeMma<D, HALVES>;
   constexpr int KT = C::KT, NB = C::NB, R = C::R;
   extern __shared__ uint8_t smem_raw[];
@@ -111,6 +185,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kTmSFull + x), 1);
       mbar_init(bar(kTmPFull + x), 128);
+      mbar_init(bar(kTmPPart + x), 128);
       mbar_init(bar(kTmODone + x), 1);
     }
     mbar_init(bar(kTmDrain), 1);
@@ -136,10 +211,9 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
   int cx = rg.lo;
   TreeSeg sg{0, 0, 0};
   auto unit_rows = [&](int& kvh, int& r0) {  // kv head, first row and rows of the unit
-    const int rts = x.units / a.Hkv;
-    kvh = x.u / rts;
-    r0 = (x.u - kvh * rts) * R;
-    return min(R, x.s.n * a.G - r0);
+    kvh = x.h;
+    r0 = x.rt * R;
+    return min(R, (x.s.n << a.lg) - r0);
   };
   auto advance = [&]() {
     cx += sg.pe - x.p;
@@ -209,8 +283,8 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
         mbar_arrive_expect_tx(bar(kTmQFull), HALVES * C::QTILE);
 #pragma unroll
         for (int e = 0; e < HALVES * C::NH; ++e)
-          tc::tma_load_3d(base + uint32_t(e) * C::QHALF, &tm_q, (e % C::NH) * 64, kvh * a.G,
-                          x.s.q0 + (r0 + (e / C::NH) * 128) / a.G, bar(kTmQFull));
+          tc::tma_load_3d(base + uint32_t(e) * C::QHALF, &tm_q, (e % C::NH) * 64, kvh << a.lg,
+                          x.s.q0 + ((r0 + (e / C::NH) * 128) >> a.lg), bar(kTmQFull));
       }
       ++seg;
       advance();
@@ -231,13 +305,13 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
                         tc::desc_kmajor(kb + uint32_t(kk >> 2) * C::KHALF + uint32_t(kk & 3) * 32u), kIdQK, kk > 0);
       tc::commit(bar(kTmSFull + hx * NB + c % NB));
     };
-    auto pv = [&](int t, int hx, int c, bool first) {  // O (+)= P V of tile t (lane 0)
+    auto pv = [&](int t, int hx, int c, bool first, int k0, int k1) {  // O (+)= P V of tile t, keys [16 k0, 16 k1) (lane 0)
       const uint32_t vb = base + C::V0 + uint32_t(t % C::VST) * C::STAGE;
 #pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk)
+      for (int kk = k0; kk < k1; ++kk)
         tc::mma_bf16_ts(tmem + C::TO + uint32_t(hx * D), s_col(hx, c) + uint32_t(kk) * 8u,
                         tc::desc_mnmajor(vb + uint32_t(kk) * 2048u, C::KHALF), kIdPV, !first || kk > 0);
-      tc::commit(bar(kTmODone + hx));
+      if (k1 == KT / 16) tc::commit(bar(kTmODone + hx));
     };
     int t = 0, seg = 0;
     bool ok = true;
@@ -279,17 +353,22 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
           if (!(ok = warp_wait(bar(kTmPFull), c & 1, a.timeout_ns))) break;
           tc::fence_after_sync();
           if (lane == 0) {
-            pv(t + j, 0, c, j == 0);
+            pv(t + j, 0, c, j == 0, 0, KT / 16);
             tc::commit(bar(kTmVFree + sv));
           }
           __syncwarp();
         } else {
           const int ca = cnt[0] - 1, cb = cnt[1] - 1;
           if (!(ok = warp_wait(bar(kTmVFull + sv), ((t + j) / C::VST) & 1, a.timeout_ns))) break;
+          // the first half of P's keys while the softmax is at the second
+          if (!(ok = warp_wait(bar(kTmPPart), ca & 1, a.timeout_ns))) break;
+          tc::fence_after_sync();
+          if (lane == 0) pv(t + j, 0, ca, j == 0, 0, KT / 32);
+          __syncwarp();
           if (!(ok = warp_wait(bar(kTmPFull), ca & 1, a.timeout_ns))) break;
           tc::fence_after_sync();
           if (lane == 0) {
-            pv(t + j, 0, ca, j == 0);
+            pv(t + j, 0, ca, j == 0, KT / 32, KT / 16);
             if (!has_b) tc::commit(bar(kTmVFree + sv));
           }
           __syncwarp();
@@ -298,10 +377,14 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
             issue_qk(j + 1, 0, !has_b);
           }
           if (has_b) {
+            if (!(ok = warp_wait(bar(kTmPPart + 1), cb & 1, a.timeout_ns))) break;
+            tc::fence_after_sync();
+            if (lane == 0) pv(t + j, 1, cb, j == 0, 0, KT / 32);
+            __syncwarp();
             if (!(ok = warp_wait(bar(kTmPFull + 1), cb & 1, a.timeout_ns))) break;
             tc::fence_after_sync();
             if (lane == 0) {
-              pv(t + j, 1, cb, j == 0);
+              pv(t + j, 1, cb, j == 0, KT / 32, KT / 16);
               tc::commit(bar(kTmVFree + sv));
             }
             __syncwarp();
@@ -346,7 +429,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       const int urow = r0 + hx * 128 + rr;  // row of the sequence's (token, head) list
       const bool row_valid = hx * 128 + rr < rows;
       const bool live = hx * 128 + quad * 32 < rows;  // the warp has a row
-      const int tok = urow / a.G, hg = urow - tok * a.G;
+      const int tok = urow >> a.lg, hg = urow - (tok << a.lg);
       const int64_t mrow = x.s.q0 + (row_valid ? tok : 0);
       float m_used = -INFINITY, l = 0.f;
       if (hx == 0 || rows > 128) {
@@ -390,7 +473,24 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
           }
           float mt = -INFINITY, alpha = 1.f, sum = 0.f;
           bool moved = false;
+          // O may be rescaled, and P counted in, only after P V of the previous tile
+          auto after_pv = [&]() {
+            if (cnt == 0) return true;
+            if (!warp_wait(bar(kTmODone + hx), (cnt - 1) & 1, a.timeout_ns)) return false;
+            tc::fence_after_sync();
+            if (live && moved && j > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c) tc::tmem_scale8(tO + uint32_t(c) * 8u, alpha);
+            }
+            return true;
+          };
           if (live) {
+            uint32_t seen[KT / 32];
+            if (tree) {
+#pragma unroll
+              for (int w = 0; w < KT / 32; ++w)
+                seen[w] = row_valid ? tree_seen32(a, mrow, n, key0 + w * 32 - c0) : 0u;
+            }
             if (!(ok = warp_wait(bar(kTmSFull + hx * NB + cnt % NB), (cnt / NB) & 1, a.timeout_ns))) break;
             tc::fence_after_sync();
             const uint32_t tS = tl + uint32_t((hx * NB + cnt % NB) * KT);
@@ -402,11 +502,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
               tc::tmem_ld128(tS, s);
             if (tree) {
 #pragma unroll
-              for (int w = 0; w < KT / 32; ++w) {
-                const uint32_t seen = row_valid ? tree_seen32(a, mrow, n, key0 + w * 32 - c0) : 0u;
-#pragma unroll
-                for (int c = 0; c < 32; ++c) s[w * 32 + c] = (seen >> c) & 1u ? s[w * 32 + c] : -INFINITY;
-              }
+              for (int c = 0; c < KT; ++c) s[c] = (seen[c / 32] >> (c % 32)) & 1u ? s[c] : -INFINITY;
             }
             float m8[8];
 #pragma unroll
@@ -422,9 +518,15 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
               m_used = m_new;
             }
             const float mu = m_used == -INFINITY ? 0.f : m_used * cl;
+            if (HALVES == 2 && !(ok = after_pv())) break;
             float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ch = 0; ch < KT / 32; ++ch) {
+              if (HALVES == 2 && ch == KT / 64) {  // P's first half is complete
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(bar(kTmPPart + hx));
+              }
               uint32_t pw[16];
 #pragma unroll
               for (int c = ch * 32; c < ch * 32 + 32; c += 2) {
@@ -445,21 +547,8 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
             }
             sum = ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
           }
-          // O may be rescaled, and P counted in, only after P V of the previous tile
-          if (cnt > 0) {
-            if (!(ok = warp_wait(bar(kTmODone + hx), (cnt - 1) & 1, a.timeout_ns))) break;
-            tc::fence_after_sync();
-            if (live && moved && j > 0) {
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tc::tmem_ld32(tO + uint32_t(c) * 32u, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                tc::tmem_st32(tO + uint32_t(c) * 32u, o);
-              }
-            }
-          }
+          if ((HALVES == 1 || !live) && !(ok = after_pv())) break;
+          if (HALVES == 2 && !live) mbar_arrive(bar(kTmPPart + hx));
           if (live) tc::tmem_wait_st();
           l = l * alpha + sum;
           tc::fence_before_sync();
@@ -504,7 +593,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
               }
             }
         };
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (x.s.q0 + tok) * a.o_st + (kvh * a.G + hg) * a.o_sh;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (x.s.q0 + tok) * a.o_st + ((kvh << a.lg) + hg) * a.o_sh;
         auto write_row = [&](int c, const float* o, float inv) {
           if (!row_valid) return;
 #pragma unroll
@@ -551,9 +640,8 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       if (!whole && rows > hx * 128) {
         // A cut unit: the half's tiles are counted in (after a timeout too,
         // so that the counters end at zero), and the half that completes the
-        // unit merges the shares of its rows, its four warps taking turns at
-        // pieces of 32 rows x 16 dims.  The barriers are reached by all four
-        // warps whatever happened to them.
+        // unit merges the shares of its rows, its four warps together.  The
+        // barriers are reached by all four warps whatever happened to them.
         half_sync(hx);
         int* const last = reinterpret_cast<int*>(gbase + C::BAR + 8 * kTmLast) + hx;
         if (quad == 0 && lane == 0)
@@ -561,70 +649,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
         half_sync(hx);
         if (*reinterpret_cast<volatile int*>(last) && ok) {
           const int ns = rg.owner(unit0 + x.nt - 1) - wa + 1;
-          const int pieces = (min(128, rows - hx * 128) + 31) / 32 * (D / 16);
-          for (int it = quad; it < pieces; it += 4) {
-            const int d0 = it % (D / 16) * 16, r = it / (D / 16) * 32 + lane;
-            auto slot_of = [&](int k) { return share_slot(wa + k, wa) * HALVES + hx; };
-            auto pair = [&](int k) {
-              return k < ns ? __ldcg(a.sh_ml + slot_of(k) * 128 + r) : make_float2(-INFINITY, 0.f);
-            };
-            float M = -INFINITY, L = 0.f;
-            for (int k0 = 0; k0 < ns; k0 += 8) {
-              float2 ml[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) ml[k] = pair(k0 + k);
-              float mn = M;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
-              const float mu = mn == -INFINITY ? 0.f : mn;
-              L *= ex2(M - mu);
-              M = mn;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) L += ml[k].y * ex2(ml[k].x - mu);
-            }
-            const float mu = M == -INFINITY ? 0.f : M;
-            float o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 1
-            for (int k0 = 0; k0 < ns; k0 += 4) {
-              float2 ml[4];
-              float4 v[4][4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                ml[k] = pair(k0 + k);
-                const float4* src = reinterpret_cast<const float4*>(a.sh_o) +
-                                    (slot_of(min(k0 + k, ns - 1)) * (D / 4) + d0 / 4) * 128 + r;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) v[k][d] = __ldcg(src + d * 128);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (k0 + k >= ns) break;
-                const float w = ex2(ml[k].x - mu);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  o[4 * d] = fmaf(w, v[k][d].x, o[4 * d]);
-                  o[4 * d + 1] = fmaf(w, v[k][d].y, o[4 * d + 1]);
-                  o[4 * d + 2] = fmaf(w, v[k][d].z, o[4 * d + 2]);
-                  o[4 * d + 3] = fmaf(w, v[k][d].w, o[4 * d + 3]);
-                }
-              }
-            }
-            if (hx * 128 + r < rows) {
-              const int row = r0 + hx * 128 + r, tk = row / a.G;
-              const float inv = tree_inverse(a, L, c0, n, x.s.q0 + tk);
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (x.s.q0 + tk) * a.o_st +
-                                   (kvh * a.G + row - tk * a.G) * a.o_sh + d0;
-#pragma unroll
-              for (int v8 = 0; v8 < 2; ++v8)
-                reinterpret_cast<uint4*>(dst)[v8] =
-                    make_uint4(pack_bf16x2(o[8 * v8] * inv, o[8 * v8 + 1] * inv),
-                               pack_bf16x2(o[8 * v8 + 2] * inv, o[8 * v8 + 3] * inv),
-                               pack_bf16x2(o[8 * v8 + 4] * inv, o[8 * v8 + 5] * inv),
-                               pack_bf16x2(o[8 * v8 + 6] * inv, o[8 * v8 + 7] * inv));
-            }
-          }
+          tree_merge<D, HALVES>(a, x, wa, ns, hx, quad, rows);
         }
       }
       advance();
