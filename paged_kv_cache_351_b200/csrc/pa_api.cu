@@ -1029,32 +1029,45 @@ pa_status tree_plan(int32_t dt, int64_t rows, TreePlan* p) {
   return PA_OK;
 }
 
-// Header, shares (two slots per worker), their (max, denominator) pairs.
+// Header, shares (two slots per worker), their (max, denominator) pairs, the
+// cut units (at most a quarter of the workers), the number of units.
+size_t tree_ml_off(const TreePlan& p, int64_t D) { return kWsHeader + size_t(2) * p.workers * p.R * D * 4; }
+size_t tree_cut_off(const TreePlan& p, int64_t D) { return tree_ml_off(p, D) + size_t(2) * p.workers * p.R * 8; }
 size_t tree_ws_bytes(const TreePlan& p, int64_t D) {
-  return kWsHeader + align_up(size_t(2) * p.workers * p.R * D * 4, 256) + align_up(size_t(2) * p.workers * p.R * 8, 256);
+  return align_up(tree_cut_off(p, D) + size_t(p.workers) * sizeof(pa::TreeCut) + 4, 256);
+}
+
+// The merge of a list with few units, after its launch: 8 parts of the dims.
+template <typename T, int D, int R>
+pa_status run_tree_merge(const pa::TreeArgs& a, int64_t units, cudaStream_t s) {
+  constexpr int RG = R < 32 ? R : 32;
+  const int64_t rows = std::min<int64_t>(R, int64_t(a.max_q) << a.lg);
+  const dim3 grid(unsigned(units), unsigned((rows + RG - 1) / RG), 8);
+  const cudaError_t err = launch_pdl(pa::tree_merge_kernel<T, D, R>, grid, dim3(pa::kTmThreads), 0, s, true, a);
+  return err == cudaSuccess ? PA_OK : launch_status();
 }
 
 template <int D, int HALVES>
 pa_status run_tree_mma(const pa::TreeArgs& a, const TreePlan& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                       const CUtensorMap& tv, cudaStream_t s, int dev) {
+                       const CUtensorMap& tv, int64_t units, cudaStream_t s, int dev) {
   static std::atomic<size_t> smem_limit[kMaxDevices];
   using C = pa::TreeMma<D, HALVES>;
   auto kern = pa::tree_mma_kernel<D, HALVES>;
   if (!raise_smem_limit(kern, size_t(C::SMEM), dev, smem_limit)) return PA_ERR_CUDA;
   if (launch_pdl(kern, dim3(unsigned(p.workers)), dim3(C::THREADS), C::SMEM, s, true, tq, tk, tv, a) != cudaSuccess)
     return launch_status();
-  return PA_OK;
+  return a.cut ? run_tree_merge<__nv_bfloat16, D, C::R>(a, units, s) : PA_OK;
 }
 
 template <typename T, int D>
-pa_status run_tree_simt(const pa::TreeArgs& a, const TreePlan& p, cudaStream_t s, int dev) {
+pa_status run_tree_simt(const pa::TreeArgs& a, const TreePlan& p, int64_t units, cudaStream_t s, int dev) {
   static std::atomic<size_t> smem_limit[kMaxDevices];
   auto kern = pa::tree_simt_kernel<T, D>;
   constexpr size_t smem = pa::tree_simt_smem<D>();
   if (!raise_smem_limit(kern, smem, dev, smem_limit)) return PA_ERR_CUDA;
   if (launch_pdl(kern, dim3(unsigned(p.workers)), dim3(pa::kTsWarps * 32), smem, s, true, a) != cudaSuccess)
     return launch_status();
-  return PA_OK;
+  return a.cut ? run_tree_merge<T, D, pa::kTsRows>(a, units, s) : PA_OK;
 }
 
 }  // namespace
@@ -1140,16 +1153,22 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   const bool split = opts && opts->partition_tokens == 0 && opts->workspace != nullptr &&
                      opts->workspace_bytes >= tree_ws_bytes(p, D);
   a.split = split ? 1 : 0;
+  a.min_len = p.halves ? 4 : 2;
+  const int64_t units = B * Hkv * ((max_query_len * G + p.R - 1) / p.R);
   if (split) {
     char* w = static_cast<char*>(opts->workspace);
+    a.sh_o = reinterpret_cast<float4*>(w + kWsHeader);
+    a.sh_ml = reinterpret_cast<float2*>(w + tree_ml_off(p, D));
     a.cnt = reinterpret_cast<unsigned int*>(w);
-    a.sh_o = reinterpret_cast<float*>(w + kWsHeader);
-    a.sh_ml = reinterpret_cast<float2*>(w + kWsHeader + align_up(size_t(2) * p.workers * p.R * D * 4, 256));
+    if (units * 4 <= p.workers) {
+      a.cut = reinterpret_cast<pa::TreeCut*>(w + tree_cut_off(p, D));
+      a.units = reinterpret_cast<int32_t*>(a.cut + p.workers);
+    }
   }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
   cudaStream_t s = stream_of(opts);
-  if (dt == PA_F32) return D == 128 ? run_tree_simt<float, 128>(a, p, s, dev) : run_tree_simt<float, 64>(a, p, s, dev);
+  if (dt == PA_F32) return D == 128 ? run_tree_simt<float, 128>(a, p, units, s, dev) : run_tree_simt<float, 64>(a, p, units, s, dev);
 
   DeviceInfo di;
   if ((st = device_info(&di, nullptr)) != PA_OK) return st;
@@ -1169,9 +1188,9 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
     if ((st = bf16_map(&tv, v_cache->data, 4, dims, strides, box)) != PA_OK) return st;
   }
   if (D == 128)
-    return p.halves == 1 ? run_tree_mma<128, 1>(a, p, tq, tk, tv, s, dev)
-                         : run_tree_mma<128, 2>(a, p, tq, tk, tv, s, dev);
-  return p.halves == 1 ? run_tree_mma<64, 1>(a, p, tq, tk, tv, s, dev) : run_tree_mma<64, 2>(a, p, tq, tk, tv, s, dev);
+    return p.halves == 1 ? run_tree_mma<128, 1>(a, p, tq, tk, tv, units, s, dev)
+                         : run_tree_mma<128, 2>(a, p, tq, tk, tv, units, s, dev);
+  return p.halves == 1 ? run_tree_mma<64, 1>(a, p, tq, tk, tv, units, s, dev) : run_tree_mma<64, 2>(a, p, tq, tk, tv, units, s, dev);
 }
 
 pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,

@@ -15,10 +15,17 @@
 // grid take equal contiguous ranges of the flattened list of units, whatever
 // the mix of lengths; a unit counts as its tiles plus LEAD (what a unit costs
 // beside its tiles, in tiles), which stand before its first tile and hold no
-// work.  A unit cut by a range boundary leaves one share per worker
-// (output before the division, running max, denominator), and whoever counts
-// in the unit's last tiles merges the shares in worker order.  Nobody waits for anybody, the result does not depend on who came
-// last, and every counter is zero again when the launch ends.
+// work.  A unit cut by a range boundary leaves one share per worker (output
+// before the division, running max, denominator), merged in worker order, so
+// that the result does not depend on timing:
+//  * a list with many units for its workers leaves few shares a unit, and
+//    whoever counts in a unit's last tiles merges them on the spot.  Nobody
+//    waits for anybody, and every counter is zero again when the launch ends;
+//  * a list with few units (a unit for four workers or more) leaves many shares
+//    a unit, and a second launch merges them, spread over the GPU: one CTA
+//    reading the 100 shares of one sequence of 20,000 tokens alone took 80 of
+//    104 us, against 32 us in all.  Many units would pay 1 to 4 us for that
+//    launch.
 #pragma once
 
 #include "pa_common.cuh"
@@ -38,12 +45,31 @@ struct TreeArgs {
   int64_t q_st, q_sh, o_st, o_sh, bt_stride, mask_stride;
   int32_t B, T, Hkv, lg, max_nb, num_blocks, words, max_q;  // lg: log2 of the query heads per kv head
   float scale_log2;  // scale * log2(e)
+  int32_t min_len;   // least list length per worker
   int32_t split;     // 1: units may be cut between workers (shares below)
-  float* sh_o;       // shares: two slots per worker, [R][D] floats each
-  float2* sh_ml;     // [R] (running max in log2 units, denominator)
-  unsigned int* cnt; // per worker and warp (or half): tiles of the unit that starts there counted in so far
+  float4* sh_o;      // shares: two slots per worker; see tree_share
+  float2* sh_ml;     // [slot][R] (running max in log2 units, denominator)
+  unsigned int* cnt; // shares merged on the spot: per worker and warp (or half), tiles of the unit that starts
+                     // there counted in so far
+  struct TreeCut* cut;  // shares merged by a second launch (else null): by the unit's number in the list
+  int32_t* units;       // and the units in the list
   uint64_t timeout_ns;
 };
+
+// What the merge needs of a unit: its shares (0: it was not cut), the worker
+// that holds its first tile, its rows.
+struct TreeCut {
+  int ns, wa, h, rt;
+  int q0, n, c0, pad;
+};
+
+// Dims 4 d .. 4 d + 3 of row r of a share: rows side by side, in blocks of at
+// most 128, so that the threads of a warp, one row each, write and read runs.
+template <int D, int R>
+__device__ __forceinline__ float4* tree_share(const TreeArgs& a, int slot, int r, int d) {
+  constexpr int RB = R < 128 ? R : 128;
+  return a.sh_o + ((int64_t(slot) * (R / RB) + r / RB) * (D / 4) + d) * RB + r % RB;
+}
 
 // The drafted rows of sequence i (n = 0: none, or a range that does not fit).
 struct TreeSeq {
@@ -65,6 +91,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int i) {
 // the unit (LEAD, then its key tiles).
 struct TreePos {
   int i, h, rt, p;
+  int number;   // of the unit in the list (if a.cut)
   int rts, nt;  // row tiles of each kv head of the sequence (0: no drafted rows), key tiles of each unit
   TreeSeq s;
 };
@@ -95,6 +122,7 @@ __device__ __forceinline__ void tree_shape(const TreeArgs& a, TreePos& x) {
 template <int R, int KT>
 __device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreePos& x) {
   x.p = 0;
+  ++x.number;
   if (++x.rt < x.rts) return;
   x.rt = 0;
   if (++x.h < a.Hkv) return;
@@ -106,9 +134,9 @@ __device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreePos& x) {
   } while (x.rts == 0);
 }
 
-// Whole block: this worker's range [lo, hi) of the list, the list's length, and the position of lo.  smem: 40 ints.
+// Whole block: this worker's range [lo, hi) of the list, the list's length, and the position of lo.  smem: 41 ints.
 //
-// Workers past N = W / MIN_LEN (at least 1, at most the grid) get nothing: a
+// Workers past N = W / min_len (at least 1, at most the grid) get nothing: a
 // short list is cut into fewer pieces, since a share costs a write and the
 // merge a read, and no worker of the others is empty.
 struct TreeRange {
@@ -128,7 +156,7 @@ struct TreeRange {
   }
 };
 
-template <int R, int KT, int LEAD, int MIN_LEN>
+template <int R, int KT, int LEAD>
 __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   const int nthr = blockDim.x;
   const int per = (a.B + nthr - 1) / nthr;
@@ -142,9 +170,22 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   }
   int total;
   const int first = block_exclusive_scan(local, smem, &total);
+  int unit0 = 0;  // units before this thread's sequences
+  if (a.cut != nullptr) {
+    int units = 0;
+    for (int i = i0; i < i1; ++i) {
+      TreePos x;
+      x.i = i;
+      tree_shape<R, KT>(a, x);
+      units += x.rts * a.Hkv;
+    }
+    int all;
+    unit0 = block_exclusive_scan(units, smem, &all);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.units = all;
+  }
   TreeRange r;
   r.W = total;
-  r.N = max(1, min(int(gridDim.x), total / MIN_LEN));
+  r.N = max(1, min(int(gridDim.x), total / a.min_len));
   r.per = total / r.N;
   r.rem = total - r.per * r.N;
   const int w = min(int(blockIdx.x), r.N);
@@ -155,7 +196,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   for (int e = 0; e < 2; ++e) {
     const int b = e == 0 ? r.lo : r.hi;
     if (b < r.W && b >= first && b < first + local) {
-      int base = first;
+      int base = first, units = unit0;
       for (int i = i0; i < i1; ++i) {
         TreePos x;
         x.i = i;
@@ -167,9 +208,11 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
           smem[32 + 4 * e + 1] = off / len;
           smem[32 + 4 * e + 2] = a.split ? off % len : 0;
           smem[32 + 4 * e + 3] = a.split ? 0 : off % len;
+          if (e == 0) smem[40] = units + off / len;
           break;
         }
         base += t;
+        units += x.rts * a.Hkv;
       }
     }
   }
@@ -177,6 +220,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   if (r.lo < r.W) {
     r.at.i = smem[32];
     r.at.p = smem[34];
+    r.at.number = smem[40];
     tree_shape<R, KT>(a, r.at);
     r.at.h = smem[33] / r.at.rts;
     r.at.rt = smem[33] - r.at.h * r.at.rts;
@@ -185,6 +229,14 @@ __device__ __forceinline__ TreeRange tree_range(const TreeArgs& a, int* smem) {
   if (r.hi < r.W) r.hi -= smem[39];
   __syncthreads();
   return r;
+}
+
+// For the second launch, by one thread of a worker at each unit that starts in
+// its range: whether it is cut.
+__device__ __forceinline__ TreeCut tree_cut(const TreeRange& rg, const TreePos& x, const TreeSeg& g, int unit0) {
+  const bool cut = g.e < x.nt;
+  return TreeCut{cut ? rg.owner(unit0 + x.nt - 1) - int(blockIdx.x) + 1 : 0, int(blockIdx.x), x.h, x.rt,
+                 x.s.q0, x.s.n, x.s.c0, 0};
 }
 
 // Bits of the 32 drafted keys u0 .. u0 + 31 that row `row` sees (u0 may be
@@ -225,7 +277,6 @@ constexpr int kTsRows = 16;
 constexpr int kTsKeys = 32;
 constexpr int kTsWarps = 4;
 constexpr int kTsLead = 1;
-constexpr int kTsMinLen = 2;
 
 template <int D>
 constexpr size_t tree_simt_smem() {
@@ -244,7 +295,7 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 
   pdl_wait();
   pdl_launch_dependents();
-  const TreeRange rg = tree_range<kTsRows, kTsKeys, kTsLead, kTsMinLen>(a, scratch);
+  const TreeRange rg = tree_range<kTsRows, kTsKeys, kTsLead>(a, scratch);
   TreePos x = rg.at;
   const uint4* kc = static_cast<const uint4*>(a.kc);
   const uint4* vc = static_cast<const uint4*>(a.vc);
@@ -364,21 +415,23 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int k = 16; k > 0; k >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
 
     // ---- the segment's result: rows of the output, or a share of a cut unit ----
-    const bool whole = sg.b == 0 && sg.e == x.nt;
+    const bool whole = sg.e - sg.b == x.nt;
     const int unit0 = cx - x.p + kTsLead;  // the unit's first tile in the list
+    if (a.cut != nullptr && threadIdx.x == 0 && sg.b == 0) a.cut[x.number] = tree_cut(rg, x, sg, unit0);
     bool write = whole;
     if (!whole) {
-      const int wa = rg.owner(unit0);
-      const int64_t slot = share_slot(blockIdx.x, wa);
+      const int slot = 2 * int(blockIdx.x) + (sg.b == 0);
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
-        if (warp * RW + r >= rows) continue;
-        const int64_t row = slot * kTsRows + warp * RW + r;
+        const int row = warp * RW + r;
+        if (row >= rows) continue;
+        float* dst = reinterpret_cast<float*>(tree_share<D, kTsRows>(a, slot, row, lane * PER / 4)) + lane * PER % 4;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) __stcg(a.sh_o + row * D + lane * PER + e, o[r][e]);
-        if (lane == 0) a.sh_ml[row] = make_float2(m[r], l[r]);
+        for (int e = 0; e < PER; ++e) __stcg(dst + e, o[r][e]);
+        if (lane == 0) __stcg(a.sh_ml + slot * kTsRows + row, make_float2(m[r], l[r]));
       }
-      write = share_done(a.cnt + wa * kTsWarps + warp, sg.e - sg.b, x.nt);
+      const int wa = a.cut == nullptr ? rg.owner(unit0) : 0;
+      write = a.cut == nullptr && share_done(a.cnt + wa * kTsWarps + warp, sg.e - sg.b, x.nt);
       if (write) {
         // Lane t holds the (max, denominator) pair of share k0 + t and turns
         // it into a weight; the weights are broadcast while every lane adds
@@ -407,7 +460,8 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 #pragma unroll 8
             for (int t = 0; t < nk; ++t) {
               const float w = __shfl_sync(0xffffffffu, wl, t);
-              const float* src = a.sh_o + (share_slot(wa + k0 + t, wa) * kTsRows + row0) * D + lane * PER;
+              const float* src = reinterpret_cast<const float*>(tree_share<D, kTsRows>(
+                                     a, int(share_slot(wa + k0 + t, wa)), int(row0), lane * PER / 4)) + lane * PER % 4;
 #pragma unroll
               for (int e = 0; e < PER; ++e) o[r][e] = fmaf(w, __ldcg(src + e), o[r][e]);
             }
@@ -435,6 +489,91 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
     if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
     __syncthreads();  // the query rows are replaced by the next segment's
   }
+}
+
+// ---- merge by a second launch ---------------------------------------------------
+// out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over a unit's shares k.
+// Block (x, y, z): unit x, RG of its rows, the z-th part of the dims; a thread
+// holds one float4 of one row.  The 8 warps first reduce every row's maximum
+// and denominator, each over every 8th share; then they split the block's
+// dims and the shares, 8 of them in flight a thread.  Bound by latency (100
+// shares of a unit are some 4 MB in L2).
+constexpr int kTmThreads = 256;
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kTmThreads) tree_merge_kernel(const TreeArgs a) {
+  constexpr int RG = R < 32 ? R : 32, DPL = 32 / RG, UN = 8;
+  __shared__ float2 part[8][RG];
+  __shared__ float4 sum[8][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  if (int(blockIdx.x) >= *a.units) return;
+  const TreeCut c = a.cut[blockIdx.x];
+  if (c.ns == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * RG + lane % RG;
+  if (c.rt * R + int(blockIdx.y) * RG >= (c.n << a.lg)) return;  // no such rows (the whole block)
+  auto slot = [&](int k) { return 2 * (c.wa + k) + (k == 0); };
+  auto pair = [&](int k) {
+    return k < c.ns ? __ldcg(a.sh_ml + slot(k) * R + r) : make_float2(-INFINITY, 0.f);
+  };
+  float M = -INFINITY, L = 0.f;
+  for (int k0 = warp; k0 < c.ns; k0 += 32) {
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) ml[k] = pair(k0 + 8 * k);
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    L *= ex2(M - mu);
+    M = mn;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) L += ml[k].y * ex2(ml[k].x - mu);
+  }
+  if (lane < RG) part[warp][lane] = make_float2(M, L);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, part[w][lane % RG].x);
+  const float mu = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) L += part[w][lane % RG].y * ex2(part[w][lane % RG].x - mu);
+
+  // this warp's float4 of the dims, and its shares: k0 and every SPL
+  const int count = D / 4 / gridDim.z;
+  const int SPL = 8 * DPL / count, k0 = warp % SPL;
+  const int d = blockIdx.z * count + warp / SPL * DPL + lane / RG;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = k0; k < c.ns; k += UN * SPL) {
+    float4 v[UN];
+    float w[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int ku = k + u * SPL;
+      w[u] = ex2(pair(ku).x - mu);
+      v[u] = ku < c.ns ? __ldcg(tree_share<D, R>(a, slot(ku), r, d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      o.x = fmaf(w[u], v[u].x, o.x);
+      o.y = fmaf(w[u], v[u].y, o.y);
+      o.z = fmaf(w[u], v[u].z, o.z);
+      o.w = fmaf(w[u], v[u].w, o.w);
+    }
+  }
+  sum[warp][lane] = o;
+  __syncthreads();
+  if (k0 != 0) return;
+  for (int w = 1; w < SPL; ++w) {
+    const float4 y = sum[warp + w][lane];
+    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+  }
+  const int row = c.rt * R + r;
+  if (row >= (c.n << a.lg)) return;
+  const int tok = row >> a.lg;
+  const float inv = tree_inverse(a, L, c.c0, c.n, c.q0 + tok);
+  T* dst = static_cast<T*>(a.out) + int64_t(c.q0 + tok) * a.o_st + ((c.h << a.lg) + (row & ((1 << a.lg) - 1))) * a.o_sh;
+  const float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  store_out_small<T, 4>(dst + 4 * d, y);
 }
 
 // ---- accepted path --------------------------------------------------------

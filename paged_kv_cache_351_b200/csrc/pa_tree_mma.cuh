@@ -39,9 +39,8 @@ struct TreeMma {
   static constexpr int NB = HALVES == 1 ? 2 : 1;  // S buffers per half
   // A unit's cost beside its tiles, in tiles (LLaMA batch of 16-token trees,
   // 12 tiles a unit: 0.197 ms with 0, 0.172 with 1, 0.154 with 2, 0.150 with
-  // 3), and the least list length worth a worker of its own.
+  // 3).
   static constexpr int LEAD = HALVES == 1 ? 3 : 1;
-  static constexpr int MIN_LEN = 4;
   static constexpr int NH = D / 64;               // 64-dim halves of the head dimension
   static constexpr int THREADS = 128 + HALVES * 128;
   static constexpr int CTAS = HALVES == 1 ? 2 : 1;  // per SM
@@ -55,10 +54,10 @@ struct TreeMma {
   static constexpr uint32_t K0 = HALVES * QTILE;
   static constexpr uint32_t V0 = K0 + KST * STAGE;
   static constexpr uint32_t BAR = V0 + VST * STAGE;
-  static constexpr uint32_t SCAN = BAR + 256;            // 40 ints
+  static constexpr uint32_t SCAN = BAR + 256;            // 41 ints
   // [4][MAXT][4] words (see "Sanitise V"): warps of one half are at most two
   // segments apart, since a tile's products wait for all of them
-  static constexpr uint32_t NONFIN = SCAN + 160;
+  static constexpr uint32_t NONFIN = SCAN + 176;
   static constexpr uint32_t SMEM = NONFIN + 4 * MAXT * 4 * 4 + 1024;  // + alignment slack
   // TMEM columns: S buffers, then O of each half
   static constexpr uint32_t TO = HALVES * NB * KT;
@@ -106,9 +105,10 @@ __device__ __noinline__ void tree_merge(const TreeArgs& a, const TreePos x, int 
   const int r = quad % (4 / parts) * 32 + lane;
   const int dl = D / parts * (quad / (4 / parts)), dh = dl + D / parts;
   if (r / 32 >= groups) return;
-  auto slot_of = [&](int k) { return share_slot(wa + k, wa) * HALVES + hx; };
+  constexpr int R = TreeMma<D, HALVES>::R;
+  auto slot_of = [&](int k) { return int(share_slot(wa + k, wa)); };
   auto pair = [&](int k) {
-    return k < ns ? __ldcg(a.sh_ml + slot_of(k) * 128 + r) : make_float2(-INFINITY, 0.f);
+    return k < ns ? __ldcg(a.sh_ml + slot_of(k) * R + hx * 128 + r) : make_float2(-INFINITY, 0.f);
   };
   float M = -INFINITY, L = 0.f;
   for (int k0 = 0; k0 < ns; k0 += 4) {
@@ -141,7 +141,7 @@ __device__ __noinline__ void tree_merge(const TreeArgs& a, const TreePos x, int 
       for (int k = 0; k < 4; ++k) {
         const bool on = k0 + k < ns;
         w[k] = ex2(pair(k0 + k).x - mu);
-        const float4* src = reinterpret_cast<const float4*>(a.sh_o) + (slot_of(k0 + k) * (D / 4) + d0 / 4) * 128 + r;
+        const float4* src = tree_share<D, R>(a, slot_of(k0 + k), hx * 128 + r, d0 / 4);
 #pragma unroll
         for (int d = 0; d < 4; ++d) v[k][d] = on ? __ldcg(src + d * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
   }
   pdl_wait();
   pdl_launch_dependents();
-  const TreeRange rg = tree_range<R, KT, C::LEAD, C::MIN_LEN>(a, reinterpret_cast<int*>(gbase + C::SCAN));
+  const TreeRange rg = tree_range<R, KT, C::LEAD>(a, reinterpret_cast<int*>(gbase + C::SCAN));
   if (rg.lo >= rg.hi) return;  // the whole CTA: nothing allocated or in flight
   if (warp == 1) tc::tmem_alloc(bar(kTmSlot), C::TCOLS);
   tc::fence_before_sync();
@@ -559,13 +559,8 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       t += nt;
       const bool whole = nt == x.nt;
       const int unit0 = cx - x.p + C::LEAD;  // the unit's first tile in the list
-      const int wa = whole ? 0 : rg.owner(unit0);
+      if (a.cut != nullptr && sg.b == 0 && threadIdx.x == 128) a.cut[x.number] = tree_cut(rg, x, sg, unit0);
       if (live) {
-        // this row's share of a worker: float4 of dims 4 d .. 4 d + 3 at [d][row]
-        auto share_o = [&](int64_t slot, int d4) {
-          return reinterpret_cast<float4*>(a.sh_o) + ((slot * HALVES + hx) * (D / 4) + d4) * 128 + rr;
-        };
-        auto share_ml = [&](int64_t slot) { return a.sh_ml + (slot * HALVES + hx) * 128 + rr; };
         // drafted tokens with infinite or NaN elements of V, in the segment's tiles
         const int tf = max(sg.b, c0 / KT);
         uint32_t any = 0;
@@ -608,7 +603,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
         };
         if (ok) {
           tc::fence_after_sync();
-          const int64_t slot = share_slot(blockIdx.x, wa);
+          const int slot = 2 * int(blockIdx.x) + (sg.b == 0);
           const float inv = whole ? tree_inverse(a, l, c0, n, mrow) : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
@@ -625,19 +620,22 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
             } else {
 #pragma unroll
               for (int d = 0; d < 16; ++d)
-                __stcg(share_o(slot, c * 16 + d), make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]));
+                __stcg(tree_share<D, R>(a, slot, hx * 128 + rr, c * 16 + d),
+                       make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]));
             }
           }
           if (HALVES == 2 && hx == 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kTmBDone));
           }
-          if (!whole) __stcg(share_ml(slot), make_float2(m_used == -INFINITY ? -INFINITY : m_used * cl, l));
+          if (!whole)
+            __stcg(a.sh_ml + slot * R + hx * 128 + rr, make_float2(m_used == -INFINITY ? -INFINITY : m_used * cl, l));
         }
       } else if (HALVES == 2 && hx == 1 && rows > 128) {
         if (lane == 0) mbar_arrive(bar(kTmBDone));
       }
-      if (!whole && rows > hx * 128) {
+      if (!whole && rows > hx * 128 && a.cut == nullptr) {
+        const int wa = rg.owner(unit0);
         // A cut unit: the half's tiles are counted in (after a timeout too,
         // so that the counters end at zero), and the half that completes the
         // unit merges the shares of its rows, its four warps together.  The
