@@ -1123,7 +1123,7 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
   if (max_query_len > PA_TREE_MAX_QUERY) return PA_ERR_UNSUPPORTED;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || T >= (int64_t(1) << 31) || max_nb * 16 > INT32_MAX || tree_mask->shape[1] > INT32_MAX)
+  if (B > 65535 || T >= (int64_t(1) << 31) || max_nb > INT32_MAX / 16 || tree_mask->shape[1] > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;
 
@@ -1175,8 +1175,10 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (di.smem_optin < int(pa::TreeMma<128, 2>::SMEM)) return PA_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   {
+    // (the stride of a dimension of size 1 may be anything: it is never taken)
+    const int64_t sh = H > 1 ? query->stride[1] : D, st0 = T > 1 ? query->stride[0] : H * D;
     const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
-    const cuuint64_t strides[2] = {cuuint64_t(query->stride[1]) * 2, cuuint64_t(query->stride[0]) * 2};
+    const cuuint64_t strides[2] = {cuuint64_t(sh) * 2, cuuint64_t(st0) * 2};
     const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(128 / G)};
     if ((st = bf16_map(&tq, query->data, 3, dims, strides, box)) != PA_OK) return st;
   }
@@ -1207,7 +1209,7 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
   if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
   if ((st = check_rows2(accepted, PA_I32, B)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || max_nb * 16 > INT32_MAX || accepted->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || max_nb > INT32_MAX / 16 || accepted->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   pa::CommitArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -1316,6 +1318,8 @@ pa_status pa_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_heads, 
   *bytes_out = 0;
   if (partition_tokens != 0 && partition_tokens != -1)
     return partition_tokens > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+  if (num_seqs > kMaxBatch || num_heads > 8 * 1024 || max_blocks_per_seq > INT32_MAX / pa::kBS)
+    return PA_ERR_UNSUPPORTED;
   DeviceInfo di;
   pa_status st = device_info(&di, nullptr);
   if (st != PA_OK) return st;
@@ -1338,6 +1342,7 @@ pa_status pa_decode_scored(pa_tensor* out, pa_tensor* scores, const pa_tensor* q
   pa_status st = decode_prepare(out, query, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
                                 k_scale, v_scale, opts, &dc);
   if (st != PA_OK) return st;
+  if (dc.max_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
   if ((st = check_rowbuf3(scores, PA_F32, dc.B, dc.Hkv)) != PA_OK) return st;
   const int32_t part = opts ? opts->partition_tokens : 0;
   if (part > 0) return PA_ERR_UNSUPPORTED;
@@ -1412,7 +1417,7 @@ pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   if ((st = check_rowbuf3(scores_out, PA_F32, B, Hkv)) != PA_OK) return st;
   if ((st = check_rowbuf3(kept_out, PA_I32, B, Hkv)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1], dst_nb = dst_tables->shape[1];
-  if (B > 65535 || max_nb * 16 > INT32_MAX || dst_nb * 16 > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || max_nb > INT32_MAX / 16 || dst_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   // the rows are compacted out of place
   if (scores_out->data == scores->data && scores->shape[2] > 0 && scores_out->shape[2] > 0) return PA_ERR_INVALID_ARG;

@@ -288,6 +288,57 @@ def test_prepared_call_and_chain_equals_prefill():
     assert (diff <= 2 * bound(ref[0], ref[1], "bf16", 128)).all()
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 128)])
+def test_few_units_with_many_shares(dtype, D):
+    """One sequence, one kv head, a long context: tens of shares of one unit
+    (the second launch), on one workspace next to a batch of many units."""
+    a = Case(39, [(6000, 21)], 2, 1, D, dtype)
+    b = Case(40, [(60, 3)] * 40, 8, 8, D, dtype)
+    ws = a.workspace()
+    n = b.workspace().numel()
+    ws = torch.zeros(max(n, ws.numel()), dtype=torch.uint8, device=DEV)
+    ra, rb = a.ref(), b.ref()
+    for _ in range(2):
+        a.check(a.run(ws=ws), ra)
+        b.check(b.run(ws=ws), rb)
+    check_status_clean()
+    assert int(ws[: pa.PA_DECODE_WS_HEADER_BYTES].count_nonzero()) == 0
+
+
+def test_two_streams_and_a_small_workspace():
+    """Calls on two streams, each with its own workspace; a workspace below the
+    size asked for leaves the context unsplit."""
+    cases = [Case(41 + k, [(900, 9), (30, 4)], 8, 2, 128, "bf16") for k in range(2)]
+    refs = [c.ref() for c in cases]
+    devs, wss = [c.device() for c in cases], [c.workspace() for c in cases]
+    outs = [torch.full((c.T, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, d, ws, out, s in zip(cases, devs, wss, outs, streams):
+            pa.pa_tree_attention(out, d["q"], d["kc"], d["vc"], d["bt"], d["cl"], d["qs"], d["mask"], c.max_q,
+                                 c.scale, c.hk, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, out, ref in zip(cases, outs, refs):
+        c.check(out, ref)
+    small = torch.zeros(1 << 16, dtype=torch.uint8, device=DEV)
+    cases[0].check(cases[0].run(ws=small), refs[0])
+    cases[0].check(cases[0].run(ws=wss[0], part=-1), refs[0])
+    check_status_clean()
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+def test_one_row_with_any_stride(dtype, D):
+    """The stride of a dimension of size 1 is never taken."""
+    c = Case(45, [(33, 1)], 1, 1, D, dtype)
+    flat = c.q.reshape(D).to(DEV)
+    q = flat.as_strided((1, 1, D), (0, 0, 1))
+    assert q.stride()[:2] == (0, 0)
+    out = c.run(ws=c.workspace(), q=q)
+    check_status_clean()
+    c.check(out)
+
+
 def test_bad_ranges_and_blocks_are_reported():
     c = Case(31, [(10, 5), (0, 4), (30, 3)], 4, 2, 128, "bf16", sees=None)
     ref = c.ref()
