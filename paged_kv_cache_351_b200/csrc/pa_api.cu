@@ -1013,14 +1013,14 @@ struct TreePlan {
   int R, KT, workers, counters, halves;  // halves 0: the CUDA-core kernel
 };
 
-constexpr int kTreeSimtCtas = 4;  // CTAs per SM of the CUDA-core kernel (its shared memory allows 5)
+constexpr int kTreeSimtCtas = 2;  // CTAs per SM of the CUDA-core kernel
 
 pa_status tree_plan(int32_t dt, int64_t rows, TreePlan* p) {
   DeviceInfo di;
   const pa_status st = device_info(&di, nullptr);
   if (st != PA_OK) return st;
   if (dt != PA_BF16)
-    *p = TreePlan{pa::kTsRows, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps, 0};
+    *p = TreePlan{rows <= 16 ? 16 : rows <= 32 ? 32 : 64, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps, 0};
   else if (rows <= 128)
     *p = TreePlan{128, pa::TreeMma<128, 1>::KT, di.sms * pa::TreeMma<128, 1>::CTAS, 1, 1};
   else
@@ -1059,15 +1059,15 @@ pa_status run_tree_mma(const pa::TreeArgs& a, const TreePlan& p, const CUtensorM
   return a.cut ? run_tree_merge<__nv_bfloat16, D, C::R>(a, units, s) : PA_OK;
 }
 
-template <typename T, int D>
+template <int D, int RW>
 pa_status run_tree_simt(const pa::TreeArgs& a, const TreePlan& p, int64_t units, cudaStream_t s, int dev) {
   static std::atomic<size_t> smem_limit[kMaxDevices];
-  auto kern = pa::tree_simt_kernel<T, D>;
-  constexpr size_t smem = pa::tree_simt_smem<D>();
+  auto kern = pa::tree_simt_kernel<D, RW>;
+  constexpr size_t smem = pa::TreeSimt<D, RW>::SMEM;
   if (!raise_smem_limit(kern, smem, dev, smem_limit)) return PA_ERR_CUDA;
   if (launch_pdl(kern, dim3(unsigned(p.workers)), dim3(pa::kTsWarps * 32), smem, s, true, a) != cudaSuccess)
     return launch_status();
-  return a.cut ? run_tree_merge<T, D, pa::kTsRows>(a, units, s) : PA_OK;
+  return a.cut ? run_tree_merge<float, D, pa::TreeSimt<D, RW>::R>(a, units, s) : PA_OK;
 }
 
 }  // namespace
@@ -1168,7 +1168,15 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
   cudaStream_t s = stream_of(opts);
-  if (dt == PA_F32) return D == 128 ? run_tree_simt<float, 128>(a, p, units, s, dev) : run_tree_simt<float, 64>(a, p, units, s, dev);
+  if (dt == PA_F32) {
+    if (D == 128)
+      return p.R == 16   ? run_tree_simt<128, 2>(a, p, units, s, dev)
+             : p.R == 32 ? run_tree_simt<128, 4>(a, p, units, s, dev)
+                         : run_tree_simt<128, 8>(a, p, units, s, dev);
+    return p.R == 16   ? run_tree_simt<64, 2>(a, p, units, s, dev)
+           : p.R == 32 ? run_tree_simt<64, 4>(a, p, units, s, dev)
+                       : run_tree_simt<64, 8>(a, p, units, s, dev);
+  }
 
   DeviceInfo di;
   if ((st = device_info(&di, nullptr)) != PA_OK) return st;

@@ -267,63 +267,97 @@ __device__ __forceinline__ float tree_inverse(const TreeArgs& a, float l, int c0
 }
 
 // ---- CUDA-core kernel ----------------------------------------------------
-// fp32 caches: products and sums in fp32, no tensor-core rounding.  R = 16
-// query rows per CTA, four to a warp; a tile of 32 keys is staged in shared
-// memory as fp32.  Scores: lane = key, the query row broadcast from shared
-// memory (K rows padded to D + 4 floats, so that 16-byte reads of 32
-// consecutive rows touch every bank once per phase).  Weighted sum: lane =
-// D / 32 dims, the probabilities broadcast by shuffles.
-constexpr int kTsRows = 16;
+// fp32 caches: products and sums in fp32, no tensor-core rounding.  Eight warps
+// of RW query rows each; tiles of 32 keys come into two stages of shared
+// memory by asynchronous 16-byte copies, the next tile while this one is
+// computed.  Scores: lane = key, the query rows broadcast from shared memory
+// (K rows padded to D + 4 floats, so that 16-byte reads of 32 consecutive rows
+// touch every bank once per phase).  Weighted sum: lane = D / 32 dims, the
+// probabilities broadcast from shared memory.  Bound by shared-memory reads:
+// per 4 dims and key, a 16-byte read of K (or V) and one of each row's query
+// (or probability) for 4 RW products, which is why a warp takes up to 8 rows
+// (16 sequences of 2,000 tokens, trees of 20, 32 heads on 8: 1.03 ms with four
+// warps of 4 rows and no copies ahead, 0.68 with 8 rows and copies ahead, 0.66
+// with eight such warps, 16 TFLOP/s; 4 x 4,000 tokens, trees of 64, 8 heads on
+// 1: 0.35, 0.23, 0.18 ms).
 constexpr int kTsKeys = 32;
-constexpr int kTsWarps = 4;
+constexpr int kTsWarps = 8;
 constexpr int kTsLead = 1;
 
-template <int D>
-constexpr size_t tree_simt_smem() {
-  return size_t(kTsKeys * (D + 4) + kTsKeys * D + kTsRows * D) * 4 + 64 * 4;
+template <int D, int RW>
+struct TreeSimt {
+  static constexpr int R = kTsWarps * RW;
+  static constexpr int KSTR = D + 4;                                // floats per row of K in shared memory
+  static constexpr int STAGE = kTsKeys * KSTR + kTsKeys * D;        // floats: K, V
+  static constexpr int Q0 = 2 * STAGE, P0 = Q0 + R * D, S0 = P0 + kTsWarps * kTsKeys * RW;
+  static constexpr size_t SMEM = size_t(S0 + 64) * 4;
+};
+
+// 16 bytes into shared memory, asynchronously; zeros if !valid.
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
 }
 
-template <typename T, int D>
+template <int D, int RW>
 __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs a) {
-  constexpr int EPV = 16 / int(sizeof(T)), VPR = D / EPV, PER = D / 32, RW = kTsRows / kTsWarps;
+  using C = TreeSimt<D, RW>;
+  constexpr int VPR = D / 4, PER = D / 32, R = C::R;
   extern __shared__ __align__(128) unsigned char smem[];
-  float* Ks = reinterpret_cast<float*>(smem);
-  float* Vs = Ks + kTsKeys * (D + 4);
-  float* Qs = Vs + kTsKeys * D;
-  int* scratch = reinterpret_cast<int*>(Qs + kTsRows * D);
+  float* const stage0 = reinterpret_cast<float*>(smem);
+  float* const Qs = stage0 + C::Q0;
+  int* scratch = reinterpret_cast<int*>(stage0 + C::S0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* const Ps = stage0 + C::P0 + warp * kTsKeys * RW;  // [key][row]
 
   pdl_wait();
   pdl_launch_dependents();
-  const TreeRange rg = tree_range<kTsRows, kTsKeys, kTsLead>(a, scratch);
+  const TreeRange rg = tree_range<R, kTsKeys, kTsLead>(a, scratch);
   TreePos x = rg.at;
-  const uint4* kc = static_cast<const uint4*>(a.kc);
-  const uint4* vc = static_cast<const uint4*>(a.vc);
+  const float* kc = static_cast<const float*>(a.kc);
+  const float* vc = static_cast<const float*>(a.vc);
 
   for (int cx = rg.lo; cx < rg.hi;) {
     // ---- one segment: this worker's tiles of one unit ----
     const TreeSeg sg = tree_seg<kTsLead>(x, rg.hi - cx);
     if (sg.b == sg.e) {
       cx += sg.pe - x.p;
-      if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
+      if (cx < rg.hi) tree_next_unit<R, kTsKeys>(a, x);
       continue;
     }
-    const int kvh = x.h, r0 = x.rt * kTsRows, gm = (1 << a.lg) - 1;
-    const int rows = min(kTsRows, (x.s.n << a.lg) - r0);
+    const int kvh = x.h, r0 = x.rt * R, gm = (1 << a.lg) - 1;
+    const int rows = min(R, (x.s.n << a.lg) - r0);
     const int kv_len = x.s.c0 + x.s.n;
-    for (int e = threadIdx.x; e < kTsRows * VPR; e += blockDim.x) {
+    const int32_t* bt = a.bt + int64_t(x.i) * a.bt_stride;
+    auto load = [&](int p) {  // tile p into its stage; keys past the end are zeros
+      float* const Ks = stage0 + (p & 1) * C::STAGE;
+      float* const Vs = Ks + kTsKeys * C::KSTR;
+#pragma unroll 4
+      for (int e = threadIdx.x; e < kTsKeys * VPR; e += kTsWarps * 32) {
+        const int t = e / VPR, c = e % VPR, key = p * kTsKeys + t;
+        const bool valid = key < kv_len;
+        int blk = valid ? __ldg(bt + key / kBS) : 0;
+        if (unsigned(blk) >= unsigned(a.num_blocks)) {
+          flag(PA_DEV_BAD_BLOCK);
+          blk = 0;
+        }
+        const int64_t off = ((int64_t(blk) * a.Hkv + kvh) * kBS + key % kBS) * D + c * 4;
+        cp_async16(Ks + t * C::KSTR + c * 4, kc + off, valid);
+        cp_async16(Vs + t * D + c * 4, vc + off, valid);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(sg.b);
+    for (int e = threadIdx.x; e < R * VPR; e += kTsWarps * 32) {
       const int r = e / VPR, c = e % VPR;
-      float f[EPV];
-#pragma unroll
-      for (int k = 0; k < EPV; ++k) f[k] = 0.f;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
         const int tok = (r0 + r) >> a.lg, j = (r0 + r) & gm;
-        Elem<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (x.s.q0 + tok) * a.q_st +
-                                                        ((kvh << a.lg) + j) * a.q_sh + c * EPV),
-                        f);
+        f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (x.s.q0 + tok) * a.q_st +
+                                             ((kvh << a.lg) + j) * a.q_sh + c * 4);
       }
-#pragma unroll
-      for (int k = 0; k < EPV; ++k) Qs[r * D + c * EPV + k] = f[k] * a.scale_log2;
+      const float k = a.scale_log2;
+      reinterpret_cast<float4*>(Qs + r * D)[c] = make_float4(f.x * k, f.y * k, f.z * k, f.w * k);
     }
     float o[RW][PER], m[RW], l[RW];
 #pragma unroll
@@ -335,79 +369,84 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
     }
     for (int p = sg.b; p < sg.e; ++p) {
       const int key0 = p * kTsKeys;
-      __syncthreads();  // the previous tile (and the query rows) are no longer in use / are complete
-      for (int e = threadIdx.x; e < kTsKeys * VPR; e += blockDim.x) {
-        const int t = e / VPR, c = e % VPR;
-        float kf[EPV], vf[EPV];
-#pragma unroll
-        for (int k = 0; k < EPV; ++k) kf[k] = vf[k] = 0.f;
-        if (key0 + t < kv_len) {
-          int blk = __ldg(a.bt + int64_t(x.i) * a.bt_stride + (key0 + t) / kBS);
-          if (unsigned(blk) >= unsigned(a.num_blocks)) {
-            flag(PA_DEV_BAD_BLOCK);
-            blk = 0;
-          }
-          const int64_t off = ((int64_t(blk) * a.Hkv + kvh) * kBS + (key0 + t) % kBS) * VPR + c;
-          Elem<T>::unpack(__ldg(kc + off), kf);
-          Elem<T>::unpack(__ldg(vc + off), vf);
-        }
-#pragma unroll
-        for (int k = 0; k < EPV; ++k) {
-          Ks[t * (D + 4) + c * EPV + k] = kf[k];
-          Vs[t * D + c * EPV + k] = vf[k];
-        }
+      if (p + 1 < sg.e) {
+        load(p + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      __syncthreads();
-      if (warp * RW >= rows) continue;  // none of this warp's rows exist
-      float s[RW];
+      __syncthreads();  // every thread's copies of this tile, and the query rows, are there
+      if (warp * RW < rows) {
+        const float* const Ks = stage0 + (p & 1) * C::STAGE;
+        const float* const Vs = Ks + kTsKeys * C::KSTR;
+        float s[RW];
 #pragma unroll
-      for (int r = 0; r < RW; ++r) s[r] = 0.f;
-      const float4* kr = reinterpret_cast<const float4*>(Ks + lane * (D + 4));
+        for (int r = 0; r < RW; ++r) s[r] = 0.f;
+        const float4* kr = reinterpret_cast<const float4*>(Ks + lane * C::KSTR);
+        const float4* qr = reinterpret_cast<const float4*>(Qs + warp * RW * D);
 #pragma unroll 4
-      for (int d = 0; d < D / 4; ++d) {
-        const float4 k4 = kr[d];
+        for (int d = 0; d < VPR; ++d) {
+          const float4 k4 = kr[d];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float4 q4 = qr[r * VPR + d];
+            s[r] = fmaf(q4.x, k4.x, s[r]);
+            s[r] = fmaf(q4.y, k4.y, s[r]);
+            s[r] = fmaf(q4.z, k4.z, s[r]);
+            s[r] = fmaf(q4.w, k4.w, s[r]);
+          }
+        }
+        const bool tree = key0 + kTsKeys > x.s.c0;  // some keys are drafted, or past the end
+        uint32_t seen[RW];
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
-          const float4 q4 = reinterpret_cast<const float4*>(Qs + (warp * RW + r) * D)[d];
-          s[r] = fmaf(q4.x, k4.x, s[r]);
-          s[r] = fmaf(q4.y, k4.y, s[r]);
-          s[r] = fmaf(q4.z, k4.z, s[r]);
-          s[r] = fmaf(q4.w, k4.w, s[r]);
+          const int row = r0 + warp * RW + r;
+          seen[r] = 0xffffffffu;
+          if (tree)
+            seen[r] = row < (x.s.n << a.lg) ? tree_seen32(a, x.s.q0 + (row >> a.lg), x.s.n, key0 - x.s.c0) : 0u;
+          const bool vis = (seen[r] >> lane) & 1u;
+          if (!vis) s[r] = -INFINITY;
+          float mx = s[r];
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          const float mn = fmaxf(m[r], mx);
+          const float al = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+          m[r] = mn;
+          s[r] = vis ? ex2(s[r] - mn) : 0.f;
+          l[r] = l[r] * al + s[r];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[r][e] *= al;
+        }
+        if constexpr (RW == 2) {
+          *reinterpret_cast<float2*>(Ps + lane * RW) = make_float2(s[0], s[1]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < RW; r += 4)
+            *reinterpret_cast<float4*>(Ps + lane * RW + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+        }
+        __syncwarp();
+        auto weigh = [&](int t, bool masked) {
+          float v[PER];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) v[e] = Vs[t * D + lane * PER + e];
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float pt = Ps[t * RW + r];
+            if (masked && !((seen[r] >> t) & 1u)) continue;  // a masked V may hold anything
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[r][e] = fmaf(pt, v[e], o[r][e]);
+          }
+        };
+        if (!tree) {
+#pragma unroll 4
+          for (int t = 0; t < kTsKeys; ++t) weigh(t, false);
+        } else {
+          const int nk = min(kTsKeys, kv_len - key0);
+#pragma unroll 1
+          for (int t = 0; t < nk; ++t) weigh(t, true);
         }
       }
-      const bool tree = key0 + kTsKeys > x.s.c0;  // some keys are drafted, or past the end
-      uint32_t seen[RW];
-#pragma unroll
-      for (int r = 0; r < RW; ++r) {
-        const int row = r0 + warp * RW + r;
-        seen[r] = 0xffffffffu;
-        if (tree) seen[r] = row < (x.s.n << a.lg) ? tree_seen32(a, x.s.q0 + (row >> a.lg), x.s.n, key0 - x.s.c0) : 0u;
-        const bool vis = (seen[r] >> lane) & 1u;
-        if (!vis) s[r] = -INFINITY;
-        float mx = s[r];
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        const float mn = fmaxf(m[r], mx);
-        const float al = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-        m[r] = mn;
-        s[r] = vis ? ex2(s[r] - mn) : 0.f;
-        l[r] = l[r] * al + s[r];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[r][e] *= al;
-      }
-      const int nk = min(kTsKeys, kv_len - key0);
-      for (int t = 0; t < nk; ++t) {
-        float v[PER];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) v[e] = Vs[t * D + lane * PER + e];
-#pragma unroll
-        for (int r = 0; r < RW; ++r) {
-          const float pt = __shfl_sync(0xffffffffu, s[r], t);
-          if (!((seen[r] >> t) & 1u)) continue;  // a masked V may hold anything
-#pragma unroll
-          for (int e = 0; e < PER; ++e) o[r][e] = fmaf(pt, v[e], o[r][e]);
-        }
-      }
+      __syncthreads();  // the stage may be filled again
     }
 #pragma unroll
     for (int r = 0; r < RW; ++r)
@@ -425,10 +464,10 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
       for (int r = 0; r < RW; ++r) {
         const int row = warp * RW + r;
         if (row >= rows) continue;
-        float* dst = reinterpret_cast<float*>(tree_share<D, kTsRows>(a, slot, row, lane * PER / 4)) + lane * PER % 4;
+        float* dst = reinterpret_cast<float*>(tree_share<D, R>(a, slot, row, lane * PER / 4)) + lane * PER % 4;
 #pragma unroll
         for (int e = 0; e < PER; ++e) __stcg(dst + e, o[r][e]);
-        if (lane == 0) __stcg(a.sh_ml + slot * kTsRows + row, make_float2(m[r], l[r]));
+        if (lane == 0) __stcg(a.sh_ml + slot * R + row, make_float2(m[r], l[r]));
       }
       const int wa = a.cut == nullptr ? rg.owner(unit0) : 0;
       write = a.cut == nullptr && share_done(a.cnt + wa * kTsWarps + warp, sg.e - sg.b, x.nt);
@@ -442,7 +481,7 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
           if (warp * RW + r >= rows) continue;
           const int64_t row0 = warp * RW + r;
           auto pair = [&](int k) {
-            return k < ns ? __ldcg(a.sh_ml + share_slot(wa + k, wa) * kTsRows + row0) : make_float2(-INFINITY, 0.f);
+            return k < ns ? __ldcg(a.sh_ml + share_slot(wa + k, wa) * R + row0) : make_float2(-INFINITY, 0.f);
           };
           float mx = -INFINITY;
           for (int k0 = 0; k0 < ns; k0 += 32) mx = fmaxf(mx, pair(k0 + lane).x);
@@ -460,7 +499,7 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 #pragma unroll 8
             for (int t = 0; t < nk; ++t) {
               const float w = __shfl_sync(0xffffffffu, wl, t);
-              const float* src = reinterpret_cast<const float*>(tree_share<D, kTsRows>(
+              const float* src = reinterpret_cast<const float*>(tree_share<D, R>(
                                      a, int(share_slot(wa + k0 + t, wa)), int(row0), lane * PER / 4)) + lane * PER % 4;
 #pragma unroll
               for (int e = 0; e < PER; ++e) o[r][e] = fmaf(w, __ldcg(src + e), o[r][e]);
@@ -480,14 +519,13 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
         float y[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) y[e] = o[r][e] * inv;
-        store_out_small<T, PER>(static_cast<T*>(a.out) + (x.s.q0 + (row >> a.lg)) * a.o_st +
+        store_out_small<float, PER>(static_cast<float*>(a.out) + (x.s.q0 + (row >> a.lg)) * a.o_st +
                                     ((kvh << a.lg) + (row & gm)) * a.o_sh + lane * PER,
                                 y);
       }
     }
     cx += sg.pe - x.p;
-    if (cx < rg.hi) tree_next_unit<kTsRows, kTsKeys>(a, x);
-    __syncthreads();  // the query rows are replaced by the next segment's
+    if (cx < rg.hi) tree_next_unit<R, kTsKeys>(a, x);
   }
 }
 
