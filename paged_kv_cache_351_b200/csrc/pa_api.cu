@@ -1008,19 +1008,24 @@ pa_status check_rows2(const pa_tensor* t, int32_t dtype, int64_t n) {
 // Launch shape of a tree attention: R query rows per unit, KT keys per tile,
 // worker CTAs, and counters per worker.  bf16 caches run on the tensor
 // cores, in one half of 128 rows while every sequence's rows per kv head fit
-// it, else in two (see pa_tree_mma.cuh).
+// it, else in two (see pa_tree_mma.cuh).  fp32 caches: as many rows a unit as a
+// sequence has, up to 64, for their use of shared memory; but 16, spread over
+// more CTAs, where the tables hold so little (`tiles` of 16 rows x 32 keys)
+// that a call is a few tiles a CTA (5 sequences of 50 tokens, 47 rows: 42 us
+// with 64 rows, 22 with 16).
 struct TreePlan {
   int R, KT, workers, counters, halves;  // halves 0: the CUDA-core kernel
 };
 
 constexpr int kTreeSimtCtas = 2;  // CTAs per SM of the CUDA-core kernel
 
-pa_status tree_plan(int32_t dt, int64_t rows, TreePlan* p) {
+pa_status tree_plan(int32_t dt, int64_t rows, int64_t tiles, TreePlan* p) {
   DeviceInfo di;
   const pa_status st = device_info(&di, nullptr);
   if (st != PA_OK) return st;
+  const int workers = di.sms * kTreeSimtCtas;
   if (dt != PA_BF16)
-    *p = TreePlan{rows <= 16 ? 16 : rows <= 32 ? 32 : 64, pa::kTsKeys, di.sms * kTreeSimtCtas, pa::kTsWarps, 0};
+    *p = TreePlan{rows <= 16 || tiles <= 4 * workers ? 16 : rows <= 32 ? 32 : 64, pa::kTsKeys, workers, pa::kTsWarps, 0};
   else if (rows <= 128)
     *p = TreePlan{128, pa::TreeMma<128, 1>::KT, di.sms * pa::TreeMma<128, 1>::CTAS, 1, 1};
   else
@@ -1083,7 +1088,7 @@ pa_status pa_tree_attention_workspace_bytes(int32_t num_heads, int32_t num_kv_he
   const int64_t rows = int64_t(max_query_len) * (num_heads / num_kv_heads);
   for (int32_t dt : {PA_F32, PA_BF16}) {
     TreePlan p;
-    const pa_status st = tree_plan(dt, rows, &p);
+    const pa_status st = tree_plan(dt, rows, INT64_MAX, &p);
     if (st != PA_OK) return st;
     *bytes_out = std::max(*bytes_out, tree_ws_bytes(p, head_size));
   }
@@ -1128,7 +1133,8 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (B == 0 || T == 0) return PA_OK;
 
   TreePlan p;
-  if ((st = tree_plan(dt, max_query_len * G, &p)) != PA_OK) return st;
+  const int64_t tiles = B * Hkv * ((max_query_len * G + 15) / 16) * ((max_nb * 16 + 31) / 32);
+  if ((st = tree_plan(dt, max_query_len * G, tiles, &p)) != PA_OK) return st;
   // the list of units (tiles and lead) is indexed with 32 bits
   const int64_t tiles_max = B * Hkv * ((max_query_len * G + p.R - 1) / p.R) * ((max_nb * 16 + p.KT - 1) / p.KT + 8);
   if (tiles_max > INT32_MAX) return PA_ERR_UNSUPPORTED;
