@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
   auto each = [&](auto&& f) {  // f(token, key) for the run, the warp together
     if constexpr (KPT > 0) {
 #pragma unroll
-      for (int k = 0; k < KPT; ++k) f(w0 + 32 * k + lane, key[k]);
+      for (int k = 0; k < KPT; ++k)
+        if (w0 + 32 * k < s.n) f(w0 + 32 * k + lane, key[k]);  // (the warp together)
     } else {
       const int end = min(min(w0 + run, (rank + 1) * chunk), s.n);
       for (int t = w0; t < end; t += 32) f(t + lane, t + lane < end ? load(t + lane) : 0u);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
 // choice and the move, a CTA a row, measured slower on the LLaMA batch, 0.193
 // against 0.164 + 0.025 ms: the longest rows are 40 times the shortest.)
 template <int VPR>  // 16-byte vectors per row
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(256, 4) evict_move_kernel(const EvictArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int g = blockIdx.y, i = blockIdx.z;
