@@ -504,8 +504,9 @@ pa_status pa_seq_compact(pa_allocator* a, const int64_t* seq_ids, const int32_t*
     // every fresh block is taken before any old one is released: no
     // destination of the batch is a source of it
     std::vector<std::vector<int32_t>> fresh(n);
-    for (int32_t r = 0; r < n; ++r) {
+    for (int32_t r = 0; r < n; ++r)  // (memory first: a failure changes nothing)
       fresh[r].resize((static_cast<size_t>(new_lens[r]) + a->block_size - 1) / a->block_size);
+    for (int32_t r = 0; r < n; ++r) {
       for (int32_t& b : fresh[r]) {
         b = a->take_block();
         a->ref[b] = 1;

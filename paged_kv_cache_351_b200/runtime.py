@@ -215,14 +215,17 @@ class PagedKVCacheGPU:
             raise ValueError("scores_out must not be scores")
         bs = self.block_size
         src, ctx = self.alloc.block_tables(seqs, max([(n + bs - 1) // bs for n in lens] + [1]))
-        dst = self.alloc.compact(seqs, new, max([(n + bs - 1) // bs for n in new] + [1]))
+        width = max([(n + bs - 1) // bs for n in new] + [1])
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        # the uploads belong to the stream that reads them
+        # the uploads belong to the stream that reads them; all device memory
+        # is taken before the allocator changes
         with torch.cuda.stream(stream):
             kept = torch.empty(len(new), self.num_kv_heads, max(new, default=0), dtype=torch.int32, device=self.device)
-            up = [torch.from_numpy(x).to(self.device) for x in (src, ctx, dst, np.asarray(new, np.int32))]
-            pa_evict(self.k_cache, self.v_cache, up[0], up[1], scores, up[2], up[3], num_sink, num_recent, scores_out,
+            up = [torch.from_numpy(x).to(self.device) for x in (src, ctx, np.asarray(new, np.int32))]
+            dst = torch.empty(len(new), width, dtype=torch.int32, device=self.device)
+            dst.copy_(torch.from_numpy(self.alloc.compact(seqs, new, width)))
+            pa_evict(self.k_cache, self.v_cache, up[0], up[1], scores, dst, up[2], num_sink, num_recent, scores_out,
                      kept, stream=stream)
         return kept
 

@@ -3,11 +3,16 @@ oracle's on random sessions, and what the rules promise, on a store model in
 which every slot remembers the token written to it."""
 
 import random
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 
 import paged_kv_cache_351_b200 as pa
 from oracle.allocator import AllocatorError, BlockAllocator, OutOfBlocks
+
+ROOT = Path(__file__).resolve().parent.parent
 
 
 def same(c, o):
@@ -147,3 +152,37 @@ def test_refusals():
     o.add(0)
     with pytest.raises(AllocatorError):
         o.truncate(0, 1)
+
+
+def test_compact_without_host_memory_changes_nothing():
+    """A child process with no room for the second sequence's table: the call
+    is refused with PA_ERR_HOST_ALLOC and the first keeps its blocks."""
+    code = (
+        "import ctypes, resource\n"
+        "import numpy as np\n"
+        "import paged_kv_cache_351_b200 as pa\n"
+        "n = 2 << 20\n"
+        "a = pa.Allocator(2 * n + 40, 1)\n"
+        "for s, k in ((0, 10), (1, n)):\n"
+        "    a.add(s)\n"
+        "    a.append(s, k)\n"
+        "before = a.num_free(), a.block_table(0)\n"
+        "out, ids, lens = np.zeros((2, n), np.int32), np.array([0, 1]), np.array([10, n], np.int32)\n"
+        "out[:] = 0\n"
+        "libc = ctypes.CDLL(None)\n"
+        "libc.malloc.restype = ctypes.c_void_p\n"
+        "resource.setrlimit(resource.RLIMIT_AS, (1 << 20, resource.RLIM_INFINITY))\n"
+        "while libc.malloc(1 << 20):\n"
+        "    pass\n"
+        "try:\n"
+        "    pa._check(pa.library().pa_seq_compact(a._h, pa._i64p(ids), pa._i32p(lens), 2, "
+        "pa._i32p(out), n), 'pa_seq_compact')\n"
+        "    status = 0\n"
+        "except pa.PagedAttentionError as e:\n"
+        "    status = e.status\n"
+        "resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))\n"
+        "print(status, before == (a.num_free(), a.block_table(0)))\n"
+    )
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120, cwd=ROOT)
+    assert res.returncode == 0, res.stderr[-2000:]
+    assert res.stdout.split() == ["8", "True"]
