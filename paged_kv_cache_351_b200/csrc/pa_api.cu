@@ -1128,7 +1128,8 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
   if (max_query_len > PA_TREE_MAX_QUERY) return PA_ERR_UNSUPPORTED;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || T >= (int64_t(1) << 31) || max_nb > INT32_MAX / 16 || tree_mask->shape[1] > INT32_MAX)
+  if (B > 65535 || Hkv > 65535 || T >= (int64_t(1) << 31) || max_nb > INT32_MAX / 16 ||
+      tree_mask->shape[1] > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;
 
@@ -1223,7 +1224,8 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
   if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
   if ((st = check_rows2(accepted, PA_I32, B)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || max_nb > INT32_MAX / 16 || accepted->shape[1] > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || k_cache->shape[1] > 65535 || max_nb > INT32_MAX / 16 || accepted->shape[1] > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   pa::CommitArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -1431,7 +1433,7 @@ pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   if ((st = check_rowbuf3(scores_out, PA_F32, B, Hkv)) != PA_OK) return st;
   if ((st = check_rowbuf3(kept_out, PA_I32, B, Hkv)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1], dst_nb = dst_tables->shape[1];
-  if (B > 65535 || max_nb > INT32_MAX / 16 || dst_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || max_nb > INT32_MAX / 16 || dst_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   // the rows are compacted out of place
   if (scores_out->data == scores->data && scores->shape[2] > 0 && scores_out->shape[2] > 0) return PA_ERR_INVALID_ARG;

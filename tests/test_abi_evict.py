@@ -101,3 +101,12 @@ def test_evict_refuses_to_compact_scores_in_place():
 
 def test_evict_with_nothing_to_do():
     pa.pa_evict(**_evict(B=0))
+
+
+def test_evict_refuses_more_kv_heads_than_a_grid_has():
+    args = _evict(B=1, hk=65536, D=64, nb=1)
+    args.update(scores=torch.zeros(1, 65536, 1), scores_out=torch.ones(1, 65536, 1),
+                kept_out=torch.zeros(1, 65536, 1, dtype=torch.int32))
+    with pytest.raises(pa.PagedAttentionError) as e:
+        pa.pa_evict(**args)
+    assert e.value.status == UNSUPPORTED

@@ -113,3 +113,11 @@ def test_commit_refuses(change):
 
 def test_commit_with_nothing_to_do():
     pa.pa_tree_commit(**_commit(B=0), stream=0)
+
+
+def test_more_kv_heads_than_a_grid_has():
+    for fn, args in ((pa.pa_tree_attention, _tree(T=1, H=65536, hk=65536, D=64, nb=1, max_q=1)),
+                     (pa.pa_tree_commit, _commit(hk=65536, D=64, nb=1))):
+        with pytest.raises(pa.PagedAttentionError) as e:
+            fn(**args, stream=0)
+        assert e.value.status == UNSUPPORTED
