@@ -986,6 +986,10 @@ namespace {
 // tree attention and the accepted path of a tree of drafted tokens
 // ---------------------------------------------------------------------------
 
+// Most tokens of a table or a row of scores: positions a tile or a grid's
+// stride (64 CTAs of 1024 tokens on each SM) past the end still fit 32 bits.
+constexpr int64_t kMaxTokens = INT32_MAX - (1 << 24);
+
 // [B] or [B + 1] int32, contiguous.
 pa_status check_i32_vec(const pa_tensor* t, int64_t n) {
   if (t == nullptr || t->ndim != 1 || t->dtype != PA_I32 || t->shape[0] != n) return PA_ERR_INVALID_ARG;
@@ -1128,7 +1132,7 @@ pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_ten
   if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
   if (max_query_len > PA_TREE_MAX_QUERY) return PA_ERR_UNSUPPORTED;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || Hkv > 65535 || T >= (int64_t(1) << 31) || max_nb > INT32_MAX / 16 ||
+  if (B > 65535 || Hkv > 65535 || T >= (int64_t(1) << 31) || max_nb > kMaxTokens / 16 ||
       tree_mask->shape[1] > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;
@@ -1224,7 +1228,7 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
   if ((st = check_rows2(block_tables, PA_I32, B)) != PA_OK) return st;
   if ((st = check_rows2(accepted, PA_I32, B)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1];
-  if (B > 65535 || k_cache->shape[1] > 65535 || max_nb > INT32_MAX / 16 || accepted->shape[1] > INT32_MAX)
+  if (B > 65535 || k_cache->shape[1] > 65535 || max_nb > kMaxTokens / 16 || accepted->shape[1] > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   pa::CommitArgs a;
@@ -1272,7 +1276,7 @@ pa_status check_rowbuf3(const pa_tensor* t, int32_t dtype, int64_t n0, int64_t n
   if (t->data == nullptr || (reinterpret_cast<uintptr_t>(t->data) & 3u) || (t->shape[2] > 1 && t->stride[2] != 1) ||
       (n1 > 1 && t->stride[1] < t->shape[2]) || (n0 > 1 && t->stride[0] < t->shape[2]))
     return PA_ERR_INVALID_ARG;
-  return t->shape[2] > INT32_MAX ? PA_ERR_UNSUPPORTED : PA_OK;
+  return t->shape[2] > kMaxTokens ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
 // Chooses the tokens of rows of at most n_max.  Up to 2048: one CTA of 256
@@ -1334,7 +1338,7 @@ pa_status pa_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_heads, 
   *bytes_out = 0;
   if (partition_tokens != 0 && partition_tokens != -1)
     return partition_tokens > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
-  if (num_seqs > kMaxBatch || num_heads > 8 * 1024 || max_blocks_per_seq > INT32_MAX / pa::kBS)
+  if (num_seqs > kMaxBatch || num_heads > 8 * 1024 || max_blocks_per_seq > kMaxTokens / pa::kBS)
     return PA_ERR_UNSUPPORTED;
   DeviceInfo di;
   pa_status st = device_info(&di, nullptr);
@@ -1358,7 +1362,7 @@ pa_status pa_decode_scored(pa_tensor* out, pa_tensor* scores, const pa_tensor* q
   pa_status st = decode_prepare(out, query, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
                                 k_scale, v_scale, opts, &dc);
   if (st != PA_OK) return st;
-  if (dc.max_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
+  if (dc.max_nb > kMaxTokens / 16) return PA_ERR_UNSUPPORTED;
   if ((st = check_rowbuf3(scores, PA_F32, dc.B, dc.Hkv)) != PA_OK) return st;
   const int32_t part = opts ? opts->partition_tokens : 0;
   if (part > 0) return PA_ERR_UNSUPPORTED;
@@ -1433,7 +1437,7 @@ pa_status pa_evict(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   if ((st = check_rowbuf3(scores_out, PA_F32, B, Hkv)) != PA_OK) return st;
   if ((st = check_rowbuf3(kept_out, PA_I32, B, Hkv)) != PA_OK) return st;
   const int64_t max_nb = block_tables->shape[1], dst_nb = dst_tables->shape[1];
-  if (B > 65535 || Hkv > 65535 || max_nb > INT32_MAX / 16 || dst_nb > INT32_MAX / 16) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535 || max_nb > kMaxTokens / 16 || dst_nb > kMaxTokens / 16) return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
   // the rows are compacted out of place
   if (scores_out->data == scores->data && scores->shape[2] > 0 && scores_out->shape[2] > 0) return PA_ERR_INVALID_ARG;

@@ -110,3 +110,16 @@ def test_evict_refuses_more_kv_heads_than_a_grid_has():
     with pytest.raises(pa.PagedAttentionError) as e:
         pa.pa_evict(**args)
     assert e.value.status == UNSUPPORTED
+
+
+def test_tables_too_long_for_32_bit_positions():
+    """(untouched memory, so only addresses are taken)"""
+    long = torch.empty(1, (2**31 - 2**24) // 16, dtype=torch.int32)
+    scored = _scored(B=1)
+    scored.update(block_tables=long)
+    src, dst = _evict(B=1), _evict(B=1)
+    src["block_tables"], dst["dst_tables"] = long, long
+    for fn, args in ((pa.pa_decode_scored, scored), (pa.pa_evict, src), (pa.pa_evict, dst)):
+        with pytest.raises(pa.PagedAttentionError) as e:
+            fn(**args)
+        assert e.value.status == UNSUPPORTED

@@ -121,3 +121,14 @@ def test_more_kv_heads_than_a_grid_has():
         with pytest.raises(pa.PagedAttentionError) as e:
             fn(**args, stream=0)
         assert e.value.status == UNSUPPORTED
+
+
+def test_tables_too_long_for_32_bit_positions():
+    """(untouched memory, so only addresses are taken)"""
+    long = torch.empty(1, (2**31 - 2**24) // 16, dtype=torch.int32)
+    tree, commit = _tree(B=1), _commit(B=1)
+    tree["block_tables"] = commit["block_tables"] = long
+    for fn, args in ((pa.pa_tree_attention, tree), (pa.pa_tree_commit, commit)):
+        with pytest.raises(pa.PagedAttentionError) as e:
+            fn(**args, stream=0)
+        assert e.value.status == UNSUPPORTED
