@@ -26,6 +26,8 @@
 // waits (bounded) for its own copies or products in flight.
 #pragma once
 
+#include <cfloat>
+
 #include "pa_prefill.cuh"
 #include "pa_tc.cuh"
 #include "pa_tree.cuh"
@@ -408,8 +410,9 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
     const uint32_t tO = tl + C::TO + uint32_t(hx * D);
     const float cl = a.scale_log2;
     // the exponent offset moves only when a row's max exceeds it by more than
-    // 2^8, so that O is rarely rescaled (see prefill_kernel)
-    const float thr = 8.f / cl;
+    // 2^8, so that O is rarely rescaled (see prefill_kernel); finite for any
+    // scale, since a row's first maximum is compared with -infinity + thr
+    const float thr = fminf(8.f / cl, FLT_MAX);
     uint32_t* const nonfin = reinterpret_cast<uint32_t*>(gbase + C::NONFIN);
     int cnt = 0, t = 0, seg = 0;  // tiles of this half, tiles, segments
     int seg_b = 0;                // segments with a half B before this one

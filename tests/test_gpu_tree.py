@@ -339,6 +339,16 @@ def test_one_row_with_any_stride(dtype, D):
     c.check(out)
 
 
+@pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("split", [True, False])
+def test_scale_next_to_zero(dtype, D, split):
+    """The least scales weigh all seen tokens alike (8 / scale is no float)."""
+    c = Case(17, [(700, 9), (3, 40)], 4, 2, D, dtype)
+    c.scale = 1e-38
+    c.check(c.run(ws=c.workspace() if split else None))
+    check_status_clean()
+
+
 def test_bad_ranges_and_blocks_are_reported():
     c = Case(31, [(10, 5), (0, 4), (30, 3)], 4, 2, 128, "bf16", sees=None)
     ref = c.ref()
