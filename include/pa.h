@@ -37,8 +37,10 @@
  * 128), (bf16, head_size 64), (fp32, head_size 64), (fp32, head_size 128),
  * and an FP8 e4m3 cache with head_size 128 and bf16 query/output
  * (pa_reshape_and_cache_fp8, pa_decode_fp8); for multi-token attention
- * (pa_prefill) bf16 with head_size 128; num_heads / num_kv_heads in
- * {1, 2, 4, 8}.  Anything else returns PA_ERR_UNSUPPORTED.
+ * (pa_prefill) bf16 with head_size 128; tree attention as decode without
+ * FP8; scored decode as decode; the moves (commit, eviction) any cache;
+ * num_heads / num_kv_heads in {1, 2, 4, 8}.  Anything else returns
+ * PA_ERR_UNSUPPORTED.
  */
 #ifndef PA_H_
 #define PA_H_
@@ -402,6 +404,11 @@ pa_status pa_prefill(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_
  * is at least pa_tree_attention_workspace_bytes, zero-filled before its first
  * use as for pa_decode; else no split) or -1 (no split); fixed partitions are
  * PA_ERR_UNSUPPORTED.
+ * bf16: tensor cores (tcgen05), fp32 accumulation and softmax statistics,
+ * probabilities rounded to bf16 for the PV product (their sum is not), output
+ * rounded to nearest even.  fp32: fp32 throughout.  One launch, or two where
+ * few sequences and kv heads are split over many CTAs.  The result depends on
+ * the split (fp32 rounding order) but not on timing.
  * ------------------------------------------------------------------------- */
 #define PA_TREE_MAX_QUERY 1024
 pa_status pa_tree_attention(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -489,7 +496,8 @@ pa_status pa_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_heads, 
  * block_tables, dst_tables: [B, *] int32; only entries that cover
  *               context_lens[i] (K) tokens are read.  A block outside the
  *               pool sets PA_DEV_BAD_BLOCK and its rows are not moved.  A
- *               destination block must not be any sequence's source block.
+ *               destination block must not be any sequence's source block,
+ *               nor be named twice.
  * scores, scores_out: [B, H_kv, S] and [B, H_kv, S'] fp32, not overlapping.
  * keep_lens:    [B] int32.  kept_out: [B, H_kv, P] int32.
  * A sequence with context_lens[i] or keep_lens[i] below 0, more tokens than

@@ -20,10 +20,14 @@ definitions:
 * ``prefill``    — multi-token (chunked-prefill) attention: every new token
   of a sequence attends causally over its cache (gitcode repo walkthrough,
   section 2.2), in fp64.
+* ``tree``       — attention of a tree of drafted tokens and the move of its
+  accepted path (speculative decoding over the cache).
+* ``evict``      — decode that accumulates attention weights, and the choice
+  and move of the tokens that stay (bounded caches).
 * ``replay``     — applies a seeded workload's requests to the allocator and
   cache models.
 * the allocator also models prefix caching (hash-free keys: parent block and
-  token ids) and swapping to a host block pool.
+  token ids), swapping to a host block pool, truncation and compaction.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU-baseline
 leg (and its ``--impl reference`` arm) may import this package.  It shares no

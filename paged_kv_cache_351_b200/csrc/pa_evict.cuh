@@ -17,7 +17,8 @@ namespace pa {
 // The weights need the final denominator, which no page knows while it is
 // read, hence the second pass over 4 G bytes a token (a second pass over K
 // would read 64 times as much at head size 128 and G = 1).  Bound by those
-// bytes plus 8 for the score; they are mostly still in L2.  Each score has
+// bytes plus 8 for the score; they are mostly still in L2 (320,000 tokens of 8
+// kv heads, G = 4: 16 us with cold caches).  Each score has
 // one writer and a fixed order of additions, so results do not vary.
 struct AccumArgs {
   const float* logits;
@@ -344,9 +345,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
 // K/V of kept token j of (sequence, kv head) -> position j of the destination
 // table.  Pure copy.  A warp takes 32 kept tokens: lane l looks up token l's
 // source and destination rows once, then the rows go 32 / VPR at a time as
-// 16-byte vectors, four steps' K and V loads in flight.  (One kernel for the
-// choice and the move, a CTA a row, measured slower on the LLaMA batch, 0.193
-// against 0.164 + 0.025 ms: the longest rows are 40 times the shortest.)
+// 16-byte vectors, four steps' K and V loads in flight.  Bound by the loads'
+// latency: the LLaMA batch cut to half reads and writes 0.88 GB at 5.3 TB/s
+// with three CTAs per SM; four (64 registers) took the whole call from 0.201
+// to 0.194 ms.  (One kernel for the choice and the move, a CTA a row, measured
+// slower, 0.193 against 0.164 + 0.025 ms: the longest rows are 40 times the
+// shortest.)
 template <int VPR>  // 16-byte vectors per row
 __global__ void __launch_bounds__(256, 4) evict_move_kernel(const EvictArgs a) {
   pdl_wait();
