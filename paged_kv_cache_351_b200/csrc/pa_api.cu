@@ -1309,8 +1309,8 @@ pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceIn
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaError_t err;
-  if (!regs)
-    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<0, 512, 2>, a, int((n_max + C - 1) / C));
+  if (!regs)  // every warp's run rounded up to whole steps of 32 tokens (see the kernel)
+    err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<0, 512, 2>, a, int((n_max + C * 16 * 32 - 1) / (C * 16 * 32) * 32));
   else if (kpt == 32)
     err = cudaLaunchKernelEx(&cfg, pa::evict_select_kernel<32, 512, 2>, a, 0);
   else if (threads == 512)

@@ -158,7 +158,7 @@ struct SelectSmem {
 };
 
 template <int KPT, int THREADS, int CTAS>
-__global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const EvictArgs a, int chunk) {
+__global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const EvictArgs a, int warp_run) {
   namespace cg = cooperative_groups;
   __shared__ SelectSmem sm;
   cg::cluster_group cl = cg::this_cluster();
@@ -177,9 +177,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
   float* so = a.scores_out + i * a.o_sb + g * a.o_sh;
   int32_t* kept = a.kept + i * a.k_sb + g * a.k_sh;
   const int lo = s.S0, hi = s.n - s.R;  // the tokens that compete
-  // this warp's run: [w0, w0 + run)
-  const int run = KPT > 0 ? 32 * KPT : (chunk + NW - 1) / NW;
-  const int w0 = KPT > 0 ? (rank * NW + warp) * run : min(s.n, rank * chunk + warp * run);
+  // This warp's run: [w0, w0 + run).  A run is a multiple of 32 tokens
+  // (warp_run with KPT = 0), so that no step of 32 reaches into the next
+  // warp's: only tokens from n on lie past a run's end, and those neither
+  // compete nor are protected.
+  const int run = KPT > 0 ? 32 * KPT : warp_run;
+  const int w0 = (rank * NW + warp) * run;
   const unsigned int mids = unsigned(hi - lo);
   auto load = [&](int t) { return unsigned(t - lo) < mids ? score_key(__ldg(sc + t)) : 0u; };  // 0: does not compete
   uint32_t key[KPT > 0 ? KPT : 1];
@@ -193,8 +196,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
       for (int k = 0; k < KPT; ++k)
         if (w0 + 32 * k < s.n) f(w0 + 32 * k + lane, key[k]);  // (the warp together)
     } else {
-      const int end = min(min(w0 + run, (rank + 1) * chunk), s.n);
-      for (int t = w0; t < end; t += 32) f(t + lane, t + lane < end ? load(t + lane) : 0u);
+      const int end = min(w0 + run, s.n);
+      for (int t = w0; t < end; t += 32) f(t + lane, load(t + lane));
     }
   };
   for (int t = s.K + rank * THREADS + tid; t < a.So; t += C * THREADS) so[t] = 0.f;
@@ -332,8 +335,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
       stay |= tie;
     }
     const uint32_t m = __ballot_sync(0xffffffffu, stay);
-    if (stay) {
-      const int pos = done + __popc(m & below);
+    const int pos = done + __popc(m & below);
+    if (stay && pos < s.K) {  // (always, unless someone writes the scores meanwhile)
       kept[pos] = t;
       so[pos] = __ldg(sc + t);
     }
