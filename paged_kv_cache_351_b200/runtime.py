@@ -25,6 +25,13 @@ from . import (Allocator, pa_copy_blocks, pa_decode, pa_decode_cascade,
 _DT = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn}
 
 
+def _stream(stream, device) -> Optional[torch.cuda.Stream]:
+    """A stream argument (None, a torch stream or a raw handle) as torch's."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 class PagedKVCacheGPU:
     """K/V pools [num_blocks, num_kv_heads, block_size, head_size] on one device."""
 
@@ -41,8 +48,7 @@ class PagedKVCacheGPU:
         self.alloc = Allocator(num_blocks, block_size, free_order)
         self._ws = None
         self._cws = None
-        self._tws = None
-        self._sws = None
+        self._scratch = {}  # (call, stream) -> workspace
         self.k_scale = self.v_scale = None
         if dtype == "fp8":
             if k_scale is None or v_scale is None:
@@ -152,18 +158,31 @@ class PagedKVCacheGPU:
                       workspace=workspace, partition_tokens=partition_tokens, stream=stream)
         return out
 
+    def _workspace(self, call: str, nbytes: int, stream) -> Optional[torch.Tensor]:
+        """The zero-filled workspace of one kind of call on ``stream`` (the
+        current one if None), grown on demand.  Each stream has its own: it is
+        zeroed on the stream that uses it, calls on two streams may overlap,
+        and one that is outgrown goes back to its own stream's memory."""
+        if nbytes == 0:
+            return None
+        dev = self.k_cache.device
+        with torch.cuda.stream(_stream(stream, dev)):
+            key = (call, torch.cuda.current_stream(dev).cuda_stream)
+            ws = self._scratch.get(key)
+            if ws is None or ws.numel() < nbytes:
+                ws = self._scratch[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        return ws
+
     # -- speculative decoding ---------------------------------------------------------
     def tree_attention(self, out: torch.Tensor, query: torch.Tensor, block_tables: torch.Tensor,
                        context_lens: torch.Tensor, query_start: torch.Tensor, tree_mask: torch.Tensor,
                        max_query_len: int, scale: float, stream=None, workspace=None) -> torch.Tensor:
         """Attention of every sequence's drafted tokens over its cache
-        (pa_tree_attention; the drafted tokens are already written).  The
-        workspace kept here serves one stream."""
+        (pa_tree_attention; the drafted tokens are already written).  Without
+        a ``workspace``, one kept here for the stream is used."""
         if workspace is None:
             n = pa_tree_attention_workspace_bytes(query.shape[1], self.num_kv_heads, self.head_size, max_query_len)
-            if self._tws is None or self._tws.numel() < n:
-                self._tws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-            workspace = self._tws
+            workspace = self._workspace("tree_attention", n, stream)
         pa_tree_attention(out, query, self.k_cache, self.v_cache, block_tables, context_lens, query_start, tree_mask,
                           max_query_len, scale, self.num_kv_heads, workspace=workspace, stream=stream)
         return out
@@ -180,13 +199,12 @@ class PagedKVCacheGPU:
                       block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                       partition_tokens: int = 0, stream=None, workspace=None) -> torch.Tensor:
         """decode, with every cached token's attention weight added to
-        ``scores`` [B, num_kv_heads, S] (pa_decode_scored)."""
+        ``scores`` [B, num_kv_heads, S] (pa_decode_scored).  Without a
+        ``workspace``, one kept here for the stream is used."""
         if workspace is None:
             n = pa_decode_scored_workspace_bytes(query.shape[0], query.shape[1], self.num_kv_heads, self.head_size,
                                                  block_tables.shape[1], partition_tokens)
-            if self._sws is None or self._sws.numel() < n:
-                self._sws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-            workspace = self._sws
+            workspace = self._workspace("decode_scored", n, stream)
         pa_decode_scored(out, scores, query, self.k_cache, self.v_cache, block_tables, context_lens, scale,
                          self.num_kv_heads, workspace, k_scale=self.k_scale, v_scale=self.v_scale,
                          partition_tokens=partition_tokens, stream=stream)
@@ -216,8 +234,7 @@ class PagedKVCacheGPU:
         bs = self.block_size
         src, ctx = self.alloc.block_tables(seqs, max([(n + bs - 1) // bs for n in lens] + [1]))
         width = max([(n + bs - 1) // bs for n in new] + [1])
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        stream = _stream(stream, self.k_cache.device)
         # the uploads belong to the stream that reads them; all device memory
         # is taken before the allocator changes
         with torch.cuda.stream(stream):
