@@ -46,8 +46,6 @@ class PagedKVCacheGPU:
         self.k_cache = torch.empty(shape, dtype=_DT[dtype], device=self.device)
         self.v_cache = torch.empty(shape, dtype=_DT[dtype], device=self.device)
         self.alloc = Allocator(num_blocks, block_size, free_order)
-        self._ws = None
-        self._cws = None
         self._scratch = {}  # (call, stream) -> workspace
         self.k_scale = self.v_scale = None
         if dtype == "fp8":
@@ -91,18 +89,30 @@ class PagedKVCacheGPU:
         else:
             pa_reshape_and_cache(key, value, self.k_cache, self.v_cache, slots, stream=stream)
 
-    def workspace(self, num_seqs: int, num_heads: int, max_blocks: int, partition_tokens: int = 0):
-        """Split scratch for ``decode``, grown on demand and reused by every
-        call (zero-filled when allocated: its merge counters must start at
-        zero, and every call leaves them zero): decodes that may overlap on
-        the GPU (different streams) must each pass a workspace of their own."""
+    def _workspace(self, call: str, nbytes: int, stream) -> Optional[torch.Tensor]:
+        """The zero-filled workspace of one kind of call on ``stream`` (the
+        current one if None), grown on demand.  Each stream has its own: it is
+        zeroed on the stream that uses it, calls on two streams may overlap,
+        and one that is outgrown goes back to its own stream's memory."""
+        if nbytes == 0:
+            return None
+        dev = self.k_cache.device
+        with torch.cuda.stream(_stream(stream, dev)):
+            key = (call, torch.cuda.current_stream(dev).cuda_stream)
+            ws = self._scratch.get(key)
+            if ws is None or ws.numel() < nbytes:
+                ws = self._scratch[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        return ws
+
+    def workspace(self, num_seqs: int, num_heads: int, max_blocks: int, partition_tokens: int = 0, stream=None):
+        """Split scratch for ``decode`` on ``stream`` (the current one if
+        None), grown on demand and reused by every such call (zero-filled when
+        allocated: its merge counters must start at zero, and every call
+        leaves them zero): decodes that may overlap on the GPU must not share
+        one."""
         n = pa_decode_workspace_bytes(num_seqs, num_heads, self.num_kv_heads, self.head_size, max_blocks,
                                       partition_tokens)
-        if n == 0:
-            return None
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        return self._ws
+        return self._workspace("decode", n, stream)
 
     def prefix_groups(self, seqs: Sequence[int], num_heads: int):
         """Groups of consecutive batch sequences that share leading blocks
@@ -122,14 +132,13 @@ class PagedKVCacheGPU:
             gs, gb = self.alloc.prefix_groups(seqs, m)
         return gs, gb, m
 
-    def shared_workspace(self, num_seqs: int, num_heads: int, max_group_size: int, partition_tokens: int = 0):
-        """Zero-filled workspace for ``decode_shared`` (grown on demand,
-        reused by every call on one stream)."""
+    def shared_workspace(self, num_seqs: int, num_heads: int, max_group_size: int, partition_tokens: int = 0,
+                         stream=None):
+        """Zero-filled workspace for ``decode_shared`` on ``stream`` (the
+        current one if None), grown on demand and reused by every such call."""
         n = pa_decode_cascade_workspace_bytes(num_seqs, num_heads, self.num_kv_heads, self.head_size, max_group_size,
                                               partition_tokens)
-        if self._cws is None or self._cws.numel() < n:
-            self._cws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        return self._cws
+        return self._workspace("decode_shared", n, stream)
 
     def decode_shared(self, out: torch.Tensor, query: torch.Tensor, block_tables: torch.Tensor,
                       context_lens: torch.Tensor, group_start: torch.Tensor, group_blocks: torch.Tensor,
@@ -138,7 +147,7 @@ class PagedKVCacheGPU:
         """Decode with each group's shared prompt blocks read once for all
         of its samples (pa_decode_cascade)."""
         if workspace is None:
-            workspace = self.shared_workspace(query.shape[0], query.shape[1], max_group_size, partition_tokens)
+            workspace = self.shared_workspace(query.shape[0], query.shape[1], max_group_size, partition_tokens, stream)
         pa_decode_cascade(out, query, self.k_cache, self.v_cache, block_tables, context_lens, group_start,
                           group_blocks, max_group_size, scale, self.num_kv_heads, workspace,
                           partition_tokens=partition_tokens, stream=stream)
@@ -148,7 +157,7 @@ class PagedKVCacheGPU:
                context_lens: torch.Tensor, scale: float, partition_tokens: int = 0, stream=None,
                workspace=None) -> torch.Tensor:
         if workspace is None:
-            workspace = self.workspace(query.shape[0], query.shape[1], block_tables.shape[1], partition_tokens)
+            workspace = self.workspace(query.shape[0], query.shape[1], block_tables.shape[1], partition_tokens, stream)
         if self.dtype == "fp8":
             pa_decode_fp8(out, query, self.k_cache, self.v_cache, block_tables, context_lens, scale,
                           self.num_kv_heads, self.k_scale, self.v_scale, workspace=workspace,
@@ -157,21 +166,6 @@ class PagedKVCacheGPU:
             pa_decode(out, query, self.k_cache, self.v_cache, block_tables, context_lens, scale, self.num_kv_heads,
                       workspace=workspace, partition_tokens=partition_tokens, stream=stream)
         return out
-
-    def _workspace(self, call: str, nbytes: int, stream) -> Optional[torch.Tensor]:
-        """The zero-filled workspace of one kind of call on ``stream`` (the
-        current one if None), grown on demand.  Each stream has its own: it is
-        zeroed on the stream that uses it, calls on two streams may overlap,
-        and one that is outgrown goes back to its own stream's memory."""
-        if nbytes == 0:
-            return None
-        dev = self.k_cache.device
-        with torch.cuda.stream(_stream(stream, dev)):
-            key = (call, torch.cuda.current_stream(dev).cuda_stream)
-            ws = self._scratch.get(key)
-            if ws is None or ws.numel() < nbytes:
-                ws = self._scratch[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        return ws
 
     # -- speculative decoding ---------------------------------------------------------
     def tree_attention(self, out: torch.Tensor, query: torch.Tensor, block_tables: torch.Tensor,
@@ -262,12 +256,13 @@ class PagedKVCacheGPU:
         if groups is not None:
             gs, gb, mg = groups
             if workspace is None:
-                workspace = self.shared_workspace(query.shape[0], query.shape[1], mg, partition_tokens)
+                workspace = self.shared_workspace(query.shape[0], query.shape[1], mg, partition_tokens, stream)
             dec = prepare_decode_cascade(out, query, self.k_cache, self.v_cache, block_tables, context_lens, gs, gb,
                                          mg, scale, self.num_kv_heads, workspace, partition_tokens, stream=stream)
         else:
             if workspace is None:
-                workspace = self.workspace(query.shape[0], query.shape[1], block_tables.shape[1], partition_tokens)
+                workspace = self.workspace(query.shape[0], query.shape[1], block_tables.shape[1], partition_tokens,
+                                           stream)
             if self.dtype == "fp8":
                 dec = prepare_decode_fp8(out, query, self.k_cache, self.v_cache, block_tables, context_lens, scale,
                                          self.num_kv_heads, self.k_scale, self.v_scale, workspace, partition_tokens,

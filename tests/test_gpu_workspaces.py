@@ -51,8 +51,11 @@ class Call:
         self.scores = torch.rand(B, HK, bt.shape[1] * 16, generator=g, device=DEV)
         self.qs = i32(np.arange(B + 1) * self.n)
         self.mask = torch.from_numpy(pack_mask([ancestors(list(range(-1, self.n - 1)))] * B, rows, 1)).to(DEV)
-        self.bytes = (pa.pa_tree_attention_workspace_bytes(H, HK, D, self.n) if kind == "tree_attention" else
-                      pa.pa_decode_scored_workspace_bytes(B, H, HK, D, bt.shape[1]))
+        self.groups = i32(np.arange(B + 1)), i32(np.zeros(B))
+        self.bytes = {"tree_attention": lambda: pa.pa_tree_attention_workspace_bytes(H, HK, D, self.n),
+                      "decode_scored": lambda: pa.pa_decode_scored_workspace_bytes(B, H, HK, D, bt.shape[1]),
+                      "decode_shared": lambda: pa.pa_decode_cascade_workspace_bytes(B, H, HK, D, 1),
+                      }.get(kind, lambda: pa.pa_decode_workspace_bytes(B, H, HK, D, bt.shape[1]))()
         torch.cuda.synchronize()
 
     def outputs(self):
@@ -61,8 +64,16 @@ class Call:
     def __call__(self, out, scores, **kw):
         if self.kind == "tree_attention":
             self.kv.tree_attention(out, self.q, self.bt, self.cl, self.qs, self.mask, self.n, SCALE, **kw)
-        else:
+        elif self.kind == "decode_scored":
             self.kv.decode_scored(out, scores, self.q, self.bt, self.cl, SCALE, **kw)
+        elif self.kind == "decode":
+            self.kv.decode(out, self.q, self.bt, self.cl, SCALE, **kw)
+        elif self.kind == "decode_shared":
+            self.kv.decode_shared(out, self.q, self.bt, self.cl, *self.groups, 1, SCALE, **kw)
+        else:  # a prepared step that appends nothing
+            row, slots = self.q[:0, :HK], torch.empty(0, dtype=torch.int64, device=DEV)
+            self.kv.prepare_step(slots, row, row, out, self.q, self.bt, self.cl, SCALE,
+                                 groups=(*self.groups, 1) if self.kind == "shared step" else None, **kw)()
 
     def want(self):
         o = self.outputs()
@@ -84,7 +95,7 @@ def same(got, want):
     return all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-KINDS = ["tree_attention", "decode_scored"]
+KINDS = ["tree_attention", "decode_scored", "decode", "decode_shared", "step", "shared step"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -102,7 +113,7 @@ def test_first_call_on_another_stream(kind, raw):
     check_status_clean()
 
 
-@pytest.mark.parametrize("kind", ["decode_scored"])  # (tree attention's size follows from the head size alone)
+@pytest.mark.parametrize("kind", KINDS[1:])  # (tree attention's size follows from the head size alone)
 def test_growth_while_the_smaller_call_waits(kind):
     """The outgrown workspace is not handed to the current stream."""
     small, large = Call(kind, 12, 900, 8), Call(kind, 12, 900, 64)
