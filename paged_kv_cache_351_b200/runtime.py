@@ -15,7 +15,7 @@ from typing import Optional, Sequence, Tuple
 import numpy as np
 import torch
 
-from . import (Allocator, pa_copy_blocks, pa_decode, pa_decode_cascade,
+from . import (PA_DECODE_WS_HEADER_BYTES, Allocator, pa_copy_blocks, pa_decode, pa_decode_cascade,
                pa_decode_cascade_workspace_bytes, pa_decode_fp8, pa_decode_scored, pa_decode_scored_workspace_bytes,
                pa_decode_workspace_bytes, pa_evict, pa_reshape_and_cache, pa_reshape_and_cache_fp8,
                pa_tree_attention, pa_tree_attention_workspace_bytes, pa_tree_commit,
@@ -93,11 +93,18 @@ class PagedKVCacheGPU:
         """The zero-filled workspace of one kind of call on ``stream`` (the
         current one if None), grown on demand.  Each stream has its own: it is
         zeroed on the stream that uses it, calls on two streams may overlap,
-        and one that is outgrown goes back to its own stream's memory."""
+        and one that is outgrown goes back to its own stream's memory.  A call
+        that is captured into a graph gets one of the graph's own memory, whose
+        counters the graph zeroes at each replay: graphs share none with each
+        other or with calls outside, and none is freed under a graph."""
         if nbytes == 0:
             return None
         dev = self.k_cache.device
-        with torch.cuda.stream(_stream(stream, dev)):
+        with torch.cuda.device(dev), torch.cuda.stream(_stream(stream, dev)):
+            if torch.cuda.is_current_stream_capturing():
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                ws[:PA_DECODE_WS_HEADER_BYTES].zero_()  # (the rest is written before it is used)
+                return ws
             key = (call, torch.cuda.current_stream(dev).cuda_stream)
             ws = self._scratch.get(key)
             if ws is None or ws.numel() < nbytes:

@@ -147,3 +147,45 @@ def test_two_streams_at_once(kind):
     torch.cuda.synchronize()
     assert all(same(o, want) for o in got[0] + got[1])
     check_status_clean()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_calls_have_workspaces_of_their_own(kind):
+    """Two graphs over one cache, the second replayed first, on two streams at
+    once and next to calls outside; then the cache's workspace grows, and the
+    graphs replay again."""
+    c = Call(kind, 12, 900, 32)
+    want = c.want()
+    big = Call(kind, 12, 900, 64)
+    big.kv, big.bt = c.kv, c.bt
+    grown = big.want()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs, graphs = [c.outputs(), c.outputs()], []
+    for s, o in zip(streams, outs):
+        with torch.cuda.stream(s):
+            c(*c.outputs())  # (loads the kernels)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c(*o)
+        graphs.append(g)
+    dirty(c.bytes, torch.cuda.current_stream(), *streams)
+    eager, large = c.outputs(), big.outputs()
+    for again in range(3):
+        for (out, scores), _ in zip(outs, graphs):
+            out.fill_(7.0), scores.copy_(c.scores)
+        eager[1].copy_(c.scores)
+        torch.cuda.synchronize()
+        for s, g in reversed(list(zip(streams, graphs))):
+            with torch.cuda.stream(s):
+                g.replay()
+        c(*eager)
+        torch.cuda.synchronize()
+        assert same(outs[0], want) and same(outs[1], want) and same(eager, want), again
+        if again == 1:
+            for s in streams:
+                big(*large, stream=s)
+                s.synchronize()
+                assert torch.equal(large[0], grown[0])
+            dirty(c.bytes, torch.cuda.current_stream(), *streams)
+    check_status_clean()
