@@ -410,9 +410,12 @@ __global__ void __launch_bounds__(kTsWarps * 32) tree_simt_kernel(const TreeArgs
 #pragma unroll
           for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
           const float mn = fmaxf(m[r], mx);
-          const float al = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+          // no key seen so far, or only logits of -infinity, which weigh nothing
+          // beside the finite ones that may follow
+          const float mu = mn == -INFINITY ? 0.f : mn;
+          const float al = ex2(m[r] - mu);
           m[r] = mn;
-          s[r] = vis ? ex2(s[r] - mn) : 0.f;
+          s[r] = vis ? ex2(s[r] - mu) : 0.f;
           l[r] = l[r] * al + s[r];
 #pragma unroll
           for (int e = 0; e < PER; ++e) o[r][e] *= al;
