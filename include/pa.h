@@ -381,7 +381,9 @@ pa_status pa_prefill(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_
  *
  * A row that sees nothing (c_i = 0 and no bit) is zero.  A row sees itself
  * only if its own bit is set.  A row does not depend on K or V at positions
- * that it does not see, whatever they hold (NaN included).
+ * that it does not see, whatever they hold (NaN included); a logit of
+ * -infinity weighs nothing, and a row that sees a logit of NaN or +infinity,
+ * or none above -infinity, is NaN.
  *
  * out, query:   [T, H, D] of the cache's dtype, last dim contiguous, strides
  *               multiples of 16 bytes, 16-byte aligned.  Rows not covered by

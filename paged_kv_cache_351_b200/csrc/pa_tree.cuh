@@ -258,11 +258,14 @@ __device__ __forceinline__ uint32_t tree_seen32(const TreeArgs& a, int64_t row, 
   return (tree_word(a, row, n, 0) << k) | ((1u << k) - 1u);
 }
 
-// 1 / (a row's denominator); 0 for a row that sees nothing, whose output is zero.
+// 1 / (a row's denominator), which is 0 only where no logit is above
+// -infinity: NaN then (0 / 0), but 0 for a row that sees nothing, whose output
+// is zero.
 __device__ __forceinline__ float tree_inverse(const TreeArgs& a, float l, int c0, int n, int64_t row) {
-  if (l != 0.f || c0 > 0) return 1.f / l;
+  if (l != 0.f) return 1.f / l;
+  if (c0 > 0) return NAN;
   for (int w = 0; w * 32 < n; ++w)
-    if (tree_word(a, row, n, w) != 0u) return 1.f / l;
+    if (tree_word(a, row, n, w) != 0u) return NAN;
   return 0.f;
 }
 

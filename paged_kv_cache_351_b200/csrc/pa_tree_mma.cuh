@@ -112,6 +112,13 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
   return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The four softmax warps of one half.
 __device__ __forceinline__ void half_sync(int hx) { asm volatile("bar.sync %0, 128;" ::"r"(1 + hx) : "memory"); }
 
@@ -531,13 +538,27 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
             float m8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = s[k];
+            if constexpr (HALVES == 1) {
 #pragma unroll
-            for (int c = 8; c < KT; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
-            mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                       fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-            moved = __any_sync(0xffffffffu, mt > m_used + thr);
+              for (int c = 8; c < KT; ++c) m8[c & 7] = fmaxf(m8[c & 7], s[c]);
+              mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                         fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+              moved = __any_sync(0xffffffffu, mt > m_used + thr);
+            } else {
+              // A NaN goes through the maximum, since the exponentials on the
+              // FMA pipe (below) drop it.
+#pragma unroll
+              for (int c = 8; c < KT; c += 16)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  m8[k] = c + 8 + k < KT ? max3_nan(m8[k], s[c + k], s[c + 8 + k]) : max3_nan(m8[k], s[c + k], s[c + k]);
+              mt = max3_nan(max3_nan(m8[0], m8[1], m8[2]), max3_nan(m8[3], m8[4], m8[5]), max3_nan(m8[6], m8[7], m8[7]));
+              moved = __any_sync(0xffffffffu, !(mt <= m_used + thr));
+            }
             if (moved) {
-              const float m_new = fmaxf(m_used, mt);
+              float m_new = HALVES == 1 ? fmaxf(m_used, mt) : max3_nan(m_used, mt, mt);
+              // +infinity: no exponential is finite, and the row is NaN
+              if (HALVES == 2 && m_new == INFINITY) m_new = NAN;
               alpha = m_new == -INFINITY ? 1.f : ex2((m_used - m_new) * cl);  // 0 on a row's first visible tile
               m_used = m_new;
             }
@@ -579,6 +600,8 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
           mbar_arrive(bar(kTmPFull + hx));
         }
         if (ok) ok = warp_wait(bar(kTmODone + hx), (cnt - 1) & 1, a.timeout_ns);
+        // the exponentials on the FMA pipe end at 2^-126, not at 0
+        if (HALVES == 2 && m_used == -INFINITY) l = 0.f;
       }
       t += nt;
       const bool whole = nt == x.nt;
