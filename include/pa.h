@@ -459,6 +459,9 @@ pa_status pa_tree_commit(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor
  *               context_lens[i] on are left as they were.  Sums are fp32,
  *               in the order of the heads; results do not vary from run to
  *               run on the same split.
+ *               A logit of -infinity weighs nothing; a row that sees a logit
+ *               of NaN or +infinity, or none above -infinity, is NaN, and
+ *               so are its weights.
  * k_scale, v_scale: [H_kv] fp32 for an e4m3 cache (query and out bf16), NULL
  *               otherwise.
  * Other arguments and dtypes as pa_decode.  opts->workspace: required, of

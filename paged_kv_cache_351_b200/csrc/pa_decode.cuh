@@ -42,6 +42,8 @@
 //    multiply them into V.
 #pragma once
 
+#include <cfloat>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -408,7 +410,7 @@ __device__ __forceinline__ bool share_done(unsigned int* cnt, int mine, int tota
 // dims of each share's outputs; the output loads of several shares are in
 // flight at once (a long row can have tens of shares, and the merge sits at
 // the end of the launch).
-template <int D, int G>
+template <int D, int G, bool kEmptyIsNaN = false>
 __device__ __forceinline__ void merge_shares(const float* ws_o, const float* ws_lse, int64_t wa, int64_t wb,
                                              int64_t W, int64_t N, float (&acc)[G][D / 32], float (&lse)[G]) {
   constexpr int PER = D / 32;
@@ -486,10 +488,12 @@ __device__ __forceinline__ void merge_shares(const float* ws_o, const float* ws_
   }
 #pragma unroll
   for (int j = 0; j < G; ++j) {
-    const float inv = wsum[j] > 0.f ? 1.f / wsum[j] : 0.f;
+    // no weight anywhere (or none that is a number): a row of a group that
+    // attended nothing is zero, a scored row is 0 / 0, and so are its weights
+    const float inv = wsum[j] > 0.f ? 1.f / wsum[j] : kEmptyIsNaN ? NAN : 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[j][e] *= inv;
-    lse[j] = wsum[j] > 0.f ? mx[j] + logf(wsum[j]) : -INFINITY;
+    lse[j] = wsum[j] > 0.f ? mx[j] + logf(wsum[j]) : kEmptyIsNaN ? NAN : -INFINITY;
   }
 }
 
@@ -498,6 +502,10 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
   using C = DecodeCfg<Tkv, Tq, D, G>;
   using T = Tkv;
   constexpr int LPT = C::LPT, TPI = C::TPI, NT = C::NT, EPV = C::EPV, GH = C::GH, QV = C::QV, EPQ = C::EPQ;
+  // A row's running maximum before its first page.  A scored decode starts
+  // from the least finite value, so that a page of logits of -infinity weighs
+  // nothing (2^(-inf - m) = 0) and does not make the scores NaN for good.
+  constexpr float kMaxStart = CK == kScored ? -FLT_MAX : -INFINITY;
   extern __shared__ __align__(128) unsigned char smem[];
 
   const int lane = threadIdx.x & 31;
@@ -803,7 +811,7 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
           for (int mm = 0; mm < 8; ++mm)
 #pragma unroll
             for (int k = 0; k < 4; ++k) oacc[mm][k] = 0.f;
-          mh[0] = mh[1] = -INFINITY;
+          mh[0] = mh[1] = kMaxStart;
           lh[0] = lh[1] = 0.f;
         } else {
 #pragma unroll
@@ -821,7 +829,7 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
             q[j][e] = f[e] * qscale;
             o[j][e] = 0.f;
           }
-          m[j] = -INFINITY;
+          m[j] = kMaxStart;
         }
 #pragma unroll
         for (int jj = 0; jj < GH; ++jj) lpart[jj] = 0.f;
@@ -1306,9 +1314,10 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
           const bool is_tail = (seg_p0 == up0);
           const int64_t slot = 2 * wid + (is_tail ? 1 : 0);
           for_owned([&](int j, int ch, const float* f, float mj, float l, bool lse_lane) {
-            // (a group row's row that attended nothing in this segment: a
-            // zero share of weight 0)
-            const float inv = (CK != kGroup || l > 0.f) ? vscale / l : 0.f;
+            // (a group row's row that attended nothing in this segment, or a
+            // scored row's segment of logits of -infinity only: a zero share of
+            // weight 0)
+            const float inv = (CK == kPlain || (CK == kGroup ? l > 0.f : l != 0.f)) ? vscale / l : 0.f;
             float4* dst = reinterpret_cast<float4*>(a.sh_o + (slot * G + j) * D + ch * EPV);
 #pragma unroll
             for (int e4 = 0; e4 < EPV / 4; ++e4)
@@ -1322,7 +1331,7 @@ __global__ void __launch_bounds__(max_warps_for(G, 16 / int(sizeof(Tkv))) * 32, 
             constexpr int PER = D / 32;
             const int64_t wb = (unit_first + unp - 1) * nworkers / W;
             float acc[G][PER], lse_m[G];
-            merge_shares<D, G>(a.sh_o, a.sh_lse, wa, wb, W, nworkers, acc, lse_m);
+            merge_shares<D, G, CK == kScored>(a.sh_o, a.sh_lse, wa, wb, W, nworkers, acc, lse_m);
             if (!row_unit) {
               // the partition's partial, as if one worker had reduced it
               const int64_t base = (int64_t(cc.i) * H + int64_t(cc.g) * G) * a.P_max + up0 / a.part_pages;

@@ -44,13 +44,7 @@ __global__ void __launch_bounds__(256) accumulate_scores_kernel(const AccumArgs 
   if (int(blockIdx.x) * kAccTokens >= n) return;
   float lse[G];
 #pragma unroll
-  for (int j = 0; j < G; ++j) {
-    // a merge whose weights do not add up to a number (a logit of NaN or
-    // +infinity) leaves -infinity here and NaN in the output: the weights
-    // are NaN as well, not 2^infinity
-    const float x = a.lse[(int64_t(i) * a.Hkv + g) * G + j];
-    lse[j] = x == -INFINITY ? NAN : x;
-  }
+  for (int j = 0; j < G; ++j) lse[j] = a.lse[(int64_t(i) * a.Hkv + g) * G + j];
   const float* lg = a.logits + (int64_t(i) * a.Hkv + g) * a.cap * G;
   float* sc = a.scores + i * a.s_sb + g * a.s_sh;
   // four tokens a thread, their loads in flight together

@@ -1,7 +1,7 @@
-"""Scored decode over a cache with NaN or infinite keys: the weights of the
-rows that see them are NaN, as the formula says, whether a row is cut between
-CTAs or not; other rows and kv heads are right.  Tolerances: see
-test_gpu_evict."""
+"""Scored decode over a cache with NaN or infinite keys, whether a row is cut
+between CTAs or not: a NaN makes the output and the weights of its rows NaN, a
+logit of -infinity weighs nothing, and a row of nothing else is 0 / 0; other
+rows and kv heads are right.  Tolerances: see test_gpu_evict."""
 
 import numpy as np
 import pytest
@@ -19,6 +19,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("ctx,at", [([4000, 700, 5], 2345), ([40, 300, 17], 39)])
 def test_one_nan_key(dtype, D, H, hk, part, ctx, at):
     c = Case(H, ctx, H, hk, D, dtype)
+    c.vc = c.vc.clone()  # (the case's fp32 K and V are one tensor)
     want, mag, acc, add = c.ref()
     b = int(c.tables[0, at // 16])
     c.kc[b, 1, at % 16, 3] = float("nan")
@@ -32,3 +33,34 @@ def test_one_nan_key(dtype, D, H, hk, part, ctx, at):
     # everything else as without the key
     got[0, g:], s[0, 1, :ctx[0]] = want[0, g:], acc[0, 1, :ctx[0]]
     c.check(torch.from_numpy(got), torch.from_numpy(s), (want, mag, acc, add))
+
+
+@pytest.mark.parametrize("dtype,D", KINDS[:4])  # (e4m3 has no infinity)
+@pytest.mark.parametrize("H,hk", [(2, 2), (4, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("part", [0, -1])
+def test_keys_of_no_weight(dtype, D, H, hk, part):
+    """The first pages of a row (and with them whole shares), a single last
+    token, every other page; then a row of such keys only."""
+    ctx = [4000, 700, 33, 2500, 40]
+    c = Case(H + 1, ctx, H, hk, D, dtype)
+    c.vc = c.vc.clone()
+    c.q[..., 0] = c.q[..., 0].abs() + 0.25  # a key of -infinity in this dimension has that logit
+    hit = [range(3000), range(16), [32], [t for t in range(2500) if t // 16 % 2], []]
+    for i, ts in enumerate(hit):
+        for t in ts:
+            c.kc[int(c.tables[i, t // 16]), :, t % 16, 0] = float("-inf")
+    out, scores = c.run(part)
+    check_status_clean()
+    ref = c.ref()
+    c.check(out, scores, ref)
+    for i in (0, 4):  # nothing else: one cut row, one whole
+        for t in range(ctx[i]):
+            c.kc[int(c.tables[i, t // 16]), 1, t % 16, 0] = float("-inf")
+    out, scores = c.run(part)
+    check_status_clean()
+    got, s = out.double().cpu().numpy(), scores.double().cpu().numpy()
+    g = H // hk
+    for i in (0, 4):
+        assert np.isnan(got[i, g:]).all() and np.isnan(s[i, 1, :ctx[i]]).all()
+        got[i, g:], s[i, 1, :ctx[i]] = ref[0][i, g:], ref[2][i, 1, :ctx[i]]
+    c.check(torch.from_numpy(got), torch.from_numpy(s), ref)
