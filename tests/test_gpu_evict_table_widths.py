@@ -18,7 +18,7 @@ import torch
 import paged_kv_cache_351_b200 as pa
 from gpu_harness import check_status_clean
 from oracle.evict import evict
-from test_gpu_evict import DEV, Case, as_bytes
+from test_gpu_evict import DEV, KINDS, Case, as_bytes
 
 pytestmark = pytest.mark.gpu
 LEFT, RIGHT = 5, 70  # entries of the output buffers before and behind each row
@@ -28,6 +28,8 @@ def check(seed, cap, ctx, keep, hk, sink, recent, scores=None, D=64, dtype="bf16
     K = [min(k, n) for k, n in zip(keep, ctx)]
     dnb = [-(-k // 16) for k in K]
     c = Case(seed, ctx, hk, hk, D, dtype, spare=sum(dnb), S=cap)
+    if dtype == "f32":
+        c.vc = c.vc * 0.75 - 0.25  # (the case's fp32 K and V are one tensor)
     if scores is not None:
         c.scores = scores(c.scores)
     table = np.full((len(ctx), -(-cap // 16)), -1, np.int32)
@@ -113,3 +115,10 @@ def test_many_rows_on_either_side_of_every_width(cap):
     ctx[3], keep[3] = min(cap, 20_000), 1000
     ctx[149], keep[149] = 1900, 1899
     check(7, cap, ctx, keep, 2, 2, 5)
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("cap", [1000, 3000, 140_000])
+def test_every_cache_type(dtype, D, cap):
+    """K to K and V to V, for rows of every length in bytes."""
+    check(8, cap, [1000, 333, 17], [500, 333, 16], 3, 2, 20, D=D, dtype=dtype)

@@ -13,13 +13,19 @@ from test_gpu_evict import KINDS, Case
 pytestmark = pytest.mark.gpu
 
 
+def own_values(c):
+    """The case's fp32 K and V are one tensor."""
+    if c.dtype == "f32":
+        c.vc = c.vc * 0.75 - 0.25
+
+
 @pytest.mark.parametrize("dtype,D", KINDS)
 @pytest.mark.parametrize("H,hk", [(2, 2), (4, 2), (8, 2), (16, 2)])
 @pytest.mark.parametrize("part", [0, -1])
 @pytest.mark.parametrize("ctx,at", [([4000, 700, 5], 2345), ([40, 300, 17], 39)])
 def test_one_nan_key(dtype, D, H, hk, part, ctx, at):
     c = Case(H, ctx, H, hk, D, dtype)
-    c.vc = c.vc.clone()  # (the case's fp32 K and V are one tensor)
+    own_values(c)
     want, mag, acc, add = c.ref()
     b = int(c.tables[0, at // 16])
     c.kc[b, 1, at % 16, 3] = float("nan")
@@ -43,7 +49,7 @@ def test_keys_of_no_weight(dtype, D, H, hk, part):
     token, every other page; then a row of such keys only."""
     ctx = [4000, 700, 33, 2500, 40]
     c = Case(H + 1, ctx, H, hk, D, dtype)
-    c.vc = c.vc.clone()
+    own_values(c)
     c.q[..., 0] = c.q[..., 0].abs() + 0.25  # a key of -infinity in this dimension has that logit
     hit = [range(3000), range(16), [32], [t for t in range(2500) if t // 16 % 2], []]
     for i, ts in enumerate(hit):
