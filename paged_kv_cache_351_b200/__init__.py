@@ -273,6 +273,12 @@ def pa_decode_scored_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads
     return int(n.value)
 
 
+def _count(n) -> int:
+    """A number of tokens as 32 bits: no sequence has more (ctypes would take
+    a larger one modulo 2^32)."""
+    return max(-1, min(int(n), 2**31 - 1))
+
+
 def pa_evict(k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens, num_sink: int,
              num_recent: int, scores_out, kept_out, stream=None) -> None:
     """Keep ``keep_lens[i]`` tokens of each sequence (the ``num_sink`` first,
@@ -285,7 +291,7 @@ def pa_evict(k_cache, v_cache, block_tables, context_lens, scores, dst_tables, k
     outs = [_tensor(x) for x in (scores_out, kept_out)]
     with _on_device(args + (scores_out, kept_out)):
         o = _opts(stream)
-        _check(_lib_handle.pa_evict(*[ctypes.byref(t) for t in ts], int(num_sink), int(num_recent),
+        _check(_lib_handle.pa_evict(*[ctypes.byref(t) for t in ts], _count(num_sink), _count(num_recent),
                                     *[ctypes.byref(t) for t in outs], ctypes.byref(o)), "pa_evict")
 
 
@@ -485,7 +491,7 @@ def prepare_evict(k_cache, v_cache, block_tables, context_lens, scores, dst_tabl
     """pa_evict, prepared (see PreparedCall)."""
     args = (k_cache, v_cache, block_tables, context_lens, scores, dst_tables, keep_lens)
     _device_index(args + (scores_out, kept_out))
-    call = PreparedCall("pa_evict", args, [ctypes.c_int32(int(num_sink)), ctypes.c_int32(int(num_recent))],
+    call = PreparedCall("pa_evict", args, [ctypes.c_int32(_count(num_sink)), ctypes.c_int32(_count(num_recent))],
                         _opts(stream), args + (scores_out, kept_out))
     # the two outputs' descriptors go between num_recent and opts
     call._outs = [_tensor(t) for t in (scores_out, kept_out)]
