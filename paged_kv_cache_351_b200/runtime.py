@@ -224,6 +224,8 @@ class PagedKVCacheGPU:
         if len(keep) != len(seqs) or min(new, default=0) < 0 or num_sink < 0 or num_recent < 0:
             raise ValueError("one length >= 0 per sequence, num_sink and num_recent >= 0")
         # everything pa_evict would refuse, before the allocator changes
+        if len(new) > 65535:
+            raise ValueError("at most 65535 sequences in one call")
         for t, need, what in ((scores, max(lens, default=0), "scores"), (scores_out, max(new, default=0), "scores_out")):
             if (tuple(t.shape[:2]) != (len(new), self.num_kv_heads) or t.dim() != 3 or t.shape[2] < need or
                     t.dtype != torch.float32 or t.device != self.k_cache.device or t.stride(2) != 1 or

@@ -1,11 +1,26 @@
-"""Eviction through PagedKVCacheGPU: counts past 32 bits
-mean "all"."""
+"""Eviction through PagedKVCacheGPU: what the call refuses, it refuses before
+the allocator changes; counts past 32 bits mean "all"."""
 
 import pytest
 import torch
 
 import paged_kv_cache_351_b200 as pa
 from paged_kv_cache_351_b200.runtime import PagedKVCacheGPU
+
+
+def test_more_sequences_than_a_launch_has_change_nothing():
+    """(a host cache, whose memory is never touched: only the bookkeeping counts)"""
+    n = 65536
+    kv = PagedKVCacheGPU(2 * n, 1, 64, "bf16", device="cpu")
+    seqs = list(range(n))
+    for s in seqs:
+        kv.add(s)
+    kv.append(seqs, [1] * n)
+    tables = [kv.alloc.block_table(s) for s in (0, 1, n - 1)]
+    scores = torch.zeros(n, 1, 1)
+    with pytest.raises(ValueError):
+        kv.evict(seqs, [1] * n, scores, torch.ones(n, 1, 1))
+    assert [kv.alloc.block_table(s) for s in (0, 1, n - 1)] == tables and kv.alloc.num_free() == n
 
 
 @pytest.mark.parametrize("many", [2**31, 2**32, 2**32 + 1, 2**63 - 1])
