@@ -400,7 +400,7 @@ pa_status pa_prefill(pa_tensor* out, const pa_tensor* query, const pa_tensor* k_
  * tree_mask:    [T, words] int32, words >= ceil(max_query_len / 32): bit
  *               u % 32 of word u / 32 of row r is drafted token u of r's
  *               sequence.  Bits from n_i on are ignored.
- * max_query_len: host-side bound on every n_i, at most PA_TREE_MAX_QUERY.
+ * max_query_len: host-side bound on every n_i, at most T and PA_TREE_MAX_QUERY.
  * scale:        finite and > 0.  H / H_kv in {1, 2, 4, 8}.
  * opts->partition_tokens: 0 (balanced split over all SMs when the workspace
  * is at least pa_tree_attention_workspace_bytes, zero-filled before its first

@@ -18,14 +18,18 @@
 // work.  A unit cut by a range boundary leaves one share per worker (output
 // before the division, running max, denominator), merged in worker order, so
 // that the result does not depend on timing:
-//  * a list with many units for its workers leaves few shares a unit, and
-//    whoever counts in a unit's last tiles merges them on the spot.  Nobody
-//    waits for anybody, and every counter is zero again when the launch ends;
-//  * a list with few units (a unit for four workers or more) leaves many shares
-//    a unit, and a second launch merges them, spread over the GPU: one CTA
-//    reading the 100 shares of one sequence of 20,000 tokens alone took 80 of
-//    104 us, against 32 us in all.  Many units would pay 1 to 4 us for that
-//    launch.
+//  * in general whoever counts in a unit's last tiles merges them on the spot.
+//    Nobody waits for anybody, and every counter is zero again when the launch
+//    ends;
+//  * with at most a unit for every four CTAs of the grid (the host knows no
+//    lengths) a second launch merges them, spread over the GPU, since a long
+//    unit may leave a share in each of a hundred CTAs, which one CTA would
+//    read alone: 20,000 tokens of one kv head 27 us against 112 on the spot,
+//    8,000 of eight 26 against 34, fp32 8,000 of one 36 against 150.  Short
+//    contexts, of a few shares a unit, pay 1 to 4 us for that launch: 500
+//    tokens of eight kv heads 16.0 against 15.0, of 32 units 20.0 against
+//    16.3, of 72 units 24.2 against 20.0 (and 3,000 of 72 units 38.3 against
+//    35.9).
 #pragma once
 
 #include "pa_common.cuh"
@@ -276,13 +280,17 @@ __device__ __forceinline__ float tree_inverse(const TreeArgs& a, float l, int c0
 // computed.  Scores: lane = key, the query rows broadcast from shared memory
 // (K rows padded to D + 4 floats, so that 16-byte reads of 32 consecutive rows
 // touch every bank once per phase).  Weighted sum: lane = D / 32 dims, the
-// probabilities broadcast from shared memory.  Bound by shared-memory reads:
-// per 4 dims and key, a 16-byte read of K (or V) and one of each row's query
-// (or probability) for 4 RW products, which is why a warp takes up to 8 rows
-// (16 sequences of 2,000 tokens, trees of 20, 32 heads on 8: 1.03 ms with four
-// warps of 4 rows and no copies ahead, 0.68 with 8 rows and copies ahead, 0.66
-// with eight such warps, 16 TFLOP/s; 4 x 4,000 tokens, trees of 64, 8 heads on
-// 1: 0.35, 0.23, 0.18 ms).
+// probabilities broadcast from shared memory.  Per 4 dims and key, a 16-byte
+// read of K (or V) and one of each row's query (or probability) serve 4 RW
+// products, which is why a warp takes up to 8 rows.  Nothing is at its limit
+// (16 sequences of 2,000 tokens, trees of 20, 32 heads on 8: FMA pipe 33%,
+// shared-memory pipe 46% on average and 74% in the busiest SM): the time goes
+// to two block barriers per 32 keys and to waiting for shared memory with 16
+// warps an SM (2.3 cycles each per issued instruction), and a sequence's last
+// unit, of 16 of its 80 rows there, reads all keys for two of its eight warps
+// at work.  (That batch: 1.03 ms with four warps of 4 rows and no copies
+// ahead, 0.68 with 8 rows and copies ahead, 0.66 with eight such warps, 16
+// TFLOP/s; 4 x 4,000 tokens, trees of 64, 8 heads on 1: 0.35, 0.23, 0.18 ms.)
 constexpr int kTsKeys = 32;
 constexpr int kTsWarps = 8;
 constexpr int kTsLead = 1;
