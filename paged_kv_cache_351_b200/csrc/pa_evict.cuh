@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) evict_select_kernel(const Evict
     }
     const uint32_t m = __ballot_sync(0xffffffffu, stay);
     const int pos = done + __popc(m & below);
-    if (stay && pos < s.K) {  // (always, unless someone writes the scores meanwhile)
+    // (pos < K always, unless scores that are read again in every pass change
+    // meanwhile)
+    if (stay && (KPT > 0 || pos < s.K)) {
       kept[pos] = t;
       so[pos] = __ldg(sc + t);
     }
