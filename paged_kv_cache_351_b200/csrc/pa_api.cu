@@ -1282,7 +1282,9 @@ pa_status check_rowbuf3(const pa_tensor* t, int32_t dtype, int64_t n0, int64_t n
 // Chooses the tokens of rows of at most n_max.  Up to 2048: one CTA of 256
 // threads a row, 8 keys each.  Up to 131072: a cluster of CTAs of 512
 // threads, 32 keys each, or 8 each while the grid has fewer CTAs than two per
-// SM.  Longer: a cluster of 8 that reads the scores again in every pass.
+// SM.  Longer: a cluster of 8 that reads the scores again in every pass (8
+// sequences of 32 to 128 thousand tokens, 8 kv heads, the whole call: 214 us
+// with tables of 131,072 tokens, 264 with one page more).
 pa_status run_evict_select(const pa::EvictArgs& a, int64_t n_max, const DeviceInfo& di, cudaStream_t s) {
   const int64_t rows = int64_t(a.B) * a.Hkv;
   int C = 1, kpt = 8, threads = 256;
