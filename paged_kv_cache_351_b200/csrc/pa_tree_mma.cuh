@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
       const int tok = urow >> a.lg, hg = urow - (tok << a.lg);
       const int64_t mrow = x.s.q0 + (row_valid ? tok : 0);
       float m_used = -INFINITY, l = 0.f;
+      float cr = cl;  // the factor of this row's scores (log2 units)
       if (hx == 0 || rows > 128) {
         for (int j = 0; ok && j < nt; ++j, ++cnt) {
           const int key0 = (sg.b + j) * KT;
@@ -565,8 +566,15 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
               if (HALVES == 2 && m_new == INFINITY) m_new = NAN;
               alpha = m_new == -INFINITY ? 1.f : ex2((m_used - m_new) * cl);  // 0 on a row's first visible tile
               m_used = m_new;
+              // s * cl - mu (one rounding) brings out what mu was rounded by: up to
+              // 2^-24 of it, within the error of the products in s, and a factor
+              // common to the tiles of one mu; but it over- or underflows from 2^31
+              // on.  From 2^30 on two scores that differ are at least 64 apart, so
+              // that all but the largest weigh nothing, and they still do with a
+              // smaller factor that keeps mu at 2^30.
+              cr = fabsf(m_used * cl) > 1073741824.f && m_used != -INFINITY ? 1073741824.f / fabsf(m_used) : cl;
             }
-            const float mu = m_used == -INFINITY ? 0.f : m_used * cl;
+            const float mu = m_used == -INFINITY ? 0.f : m_used * cr;
             if (HALVES == 2 && !(ok = after_pv())) break;
             float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(TreeMma<D, HALVES>::THREADS, TreeMma<D, HALVES
 #pragma unroll
               for (int c = ch * 32; c < ch * 32 + 32; c += 2) {
                 float e0 = -mu, e1 = -mu;
-                ffma2(e0, e1, s[c], s[c + 1], cl, cl);  // s * cl - mu
+                ffma2(e0, e1, s[c], s[c + 1], cr, cr);  // s * cl - mu
                 // with two halves the special-function unit would be the
                 // bottleneck: a quarter of the exponentials on the FMA pipe
                 if (HALVES == 2 && !tree && ((c >> 3) & 3) == 3) {
